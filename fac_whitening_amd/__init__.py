@@ -28,12 +28,15 @@ _lib = ctypes.CDLL(LIB_PATH)
 EUCLID, DIAG, LOWRANK, CHOL_INPUT, CHOL_TWOSIDED = range(5)
 E4M3, E5M2, E2M1 = 0, 1, 2
 SCALE_TENSOR, SCALE_BLOCK128, SCALE_BLOCK16, SCALE_BLOCK512 = 0, 1, 2, 3
-BF16, FP32 = 0, 1
+BF16, FP32, FP16 = 0, 1, 2   # FP16: activation operators only
+NORM_LAYER, NORM_RMS = 0, 1
 SIDE_A, SIDE_G = 0, 1
 LAYER_TRANSIENT_STATS = 1   # statistics windows committed in one call, S in the workspace
 FLAG_NONFINITE, FLAG_SPIN_TIMEOUT = 1, 2
 TRANSFORMS = {"euclid": EUCLID, "diag": DIAG, "lowrank": LOWRANK, "chol": CHOL_INPUT, "twosided": CHOL_TWOSIDED}
 FORMATS = {"e4m3": E4M3, "e5m2": E5M2}
+NORMS = {"layer": NORM_LAYER, "rms": NORM_RMS}
+DTYPES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16}
 SCALINGS = {"tensor": SCALE_TENSOR, "block": SCALE_BLOCK128}
 STATUS = {0: "GIFT_OK", 1: "GIFT_ERR_INVALID_ARG", 2: "GIFT_ERR_WORKSPACE", 3: "GIFT_ERR_NOT_READY",
           4: "GIFT_ERR_NUMERICAL", 5: "GIFT_ERR_UNSUPPORTED", 6: "GIFT_ERR_HIP"}
@@ -49,6 +52,8 @@ EXPORTS = [
     "gift_bucket_decode_reduce", "gift_scale_sync_due", "gift_set_max_resident", "gift_layer_route",
     "gift_bucket_encode_static", "gift_group_table_bytes", "gift_group_create", "gift_group_destroy",
     "gift_group_encode", "gift_group_decode_reduce",
+    "gift_act_scale_bytes", "gift_act_save", "gift_act_restore", "gift_norm_forward", "gift_norm_workspace_bytes",
+    "gift_norm_backward", "gift_weight_grad_workspace_bytes", "gift_weight_grad",
 ]
 
 
@@ -63,6 +68,11 @@ class LayerDesc(ctypes.Structure):
     _fields_ = [("d_out", ctypes.c_int32), ("d_in", ctypes.c_int32), ("transform", ctypes.c_int32),
                 ("rank", ctypes.c_int32), ("oversample", ctypes.c_int32), ("power_iters", ctypes.c_int32),
                 ("ema_decay", ctypes.c_float), ("damping_rel", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
+class ActCkpt(ctypes.Structure):
+    _fields_ = [("d_codes", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("d_bscales", ctypes.c_void_p),
+                ("fmt", ctypes.c_int32)]
 
 
 _vp, _sz, _i32, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
@@ -118,6 +128,17 @@ _sig("gift_group_create", _i32, _i32, _P(GroupItem), _i32, _i32, _i32, _vp, _sz,
 _sig("gift_group_destroy", _i32, _vp)
 _sig("gift_group_encode", _i32, _vp, _vp)
 _sig("gift_group_decode_reduce", _i32, _vp, _vp)
+_f32 = ctypes.c_float
+_sig("gift_act_scale_bytes", _sz, _i64, _i32)
+_sig("gift_act_save", _i32, _vp, _i32, _i64, _i64, _i32, _P(ActCkpt), _vp)
+_sig("gift_act_restore", _i32, _P(ActCkpt), _i64, _i32, _vp, _i32, _i64, _vp)
+_sig("gift_norm_forward", _i32, _i32, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _i32, _f32, _vp, _i64, _vp, _vp,
+     _P(ActCkpt), _vp)
+_sig("gift_norm_workspace_bytes", _sz, _i64, _i32)
+_sig("gift_norm_backward", _i32, _i32, _vp, _i32, _i64, _vp, _i64, _P(ActCkpt), _i64, _i32, _vp, _i32, _vp, _vp, _vp,
+     _i64, _vp, _vp, _i32, _vp, _sz, _vp)
+_sig("gift_weight_grad_workspace_bytes", _sz, _i64, _i32, _i32, _i32)
+_sig("gift_weight_grad", _i32, _vp, _i32, _i64, _i32, _P(ActCkpt), _i64, _i32, _f32, _i32, _vp, _i64, _vp, _sz, _vp)
 
 
 def set_fused(enable: bool) -> bool:
@@ -528,3 +549,167 @@ class Group:
             self.close()
         except Exception:
             pass
+
+
+# -- activation operators (gift_act_*, gift_norm_*, gift_weight_grad) -----------
+# What these functions allocate (outputs not given, workspaces) comes from the
+# allocator's pool of the stream they launch on, so it may be dropped as soon
+# as the call returns; tensors the caller passes are the caller's to order.
+
+def _rows(t, what, T=None, n=None, dtype=None):
+    """Checks a [T][n] tensor with unit column stride; returns its leading dimension."""
+    if t.dim() != 2 or t.dtype not in DTYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be a [T][n] tensor of {dtype or 'bf16, fp16 or fp32'}")
+    if (T is not None and t.shape[0] != T) or (n is not None and t.shape[1] != n):
+        raise ValueError(f"{what} must have shape [{T}][{n}], not {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit column stride")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _vector(t, what, n, dtypes, device):
+    if t is None:
+        return None
+    if t.numel() != n or t.dim() != 1 or t.dtype not in dtypes or (n > 1 and t.stride(0) != 1) or t.device != device:
+        raise ValueError(f"{what} must be a dense vector of {n} {' or '.join(map(str, dtypes))} on {device}")
+    return t
+
+
+def _empty(stream, shape, dtype, device):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class ActCheckpoint:
+    """8-bit checkpoint of a [T][d] activation (gift_act_*): codes [T][ldc]
+    uint8 with ldc = d rounded up to 32, and bscales
+    [ceil(T / 8)][ceil(d / 32)][8] uint8, the biased exponent of the scale of
+    each token and 32 columns.  Buffers that are not given are allocated (on
+    `stream`'s pool); given ones are used as they are, so a checkpoint kept
+    elsewhere can be wrapped without a copy."""
+
+    def __init__(self, T: int, d: int, fmt=E4M3, codes=None, bscales=None, device="cuda", stream=None):
+        self.T, self.d, self.fmt = int(T), int(d), FORMATS.get(fmt, fmt)
+        if self.T < 0 or self.d < 1 or self.fmt not in (E4M3, E5M2):
+            raise ValueError("a checkpoint needs T >= 0, d >= 1 and the format E4M3 or E5M2")
+        nb, groups = -(-self.d // 32), -(-self.T // 8)
+        if codes is None:
+            codes = _empty(stream, (self.T, nb * 32), torch.uint8, device)
+        if bscales is None:
+            bscales = _empty(stream, (groups, nb, 8), torch.uint8, codes.device)
+        if codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[0] != self.T or codes.shape[1] < nb * 32 or (
+                codes.stride(1) != 1) or not codes.is_cuda:
+            raise ValueError(f"codes must be a uint8 [{self.T}][>= {nb * 32}] tensor on the GPU with unit column stride")
+        if bscales.dtype != torch.uint8 or bscales.numel() != groups * nb * 8 or not bscales.is_contiguous() or (
+                bscales.device != codes.device):
+            raise ValueError(f"bscales must be a contiguous uint8 [{groups}][{nb}][8] tensor beside the codes")
+        self.codes, self.bscales, self.device = codes, bscales, codes.device
+        self._c = ActCkpt(codes.data_ptr(), codes.stride(0) if self.T > 1 else codes.shape[1] // 32 * 32,
+                          bscales.data_ptr(), self.fmt)
+        self._ref = ctypes.byref(self._c)
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.bscales.numel()
+
+    def save(self, x: torch.Tensor, stream=None):
+        ld = _rows(x, "x", self.T, self.d)
+        _check(_lib.gift_act_save(x.data_ptr(), DTYPES[x.dtype], ld, self.T, self.d, self._ref, _stream(stream)),
+               "gift_act_save")
+        return self
+
+    def restore(self, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+        if out is None:
+            out = _empty(stream, (self.T, self.d), dtype, self.device)
+        ld = _rows(out, "out", self.T, self.d)
+        _check(_lib.gift_act_restore(self._ref, self.T, self.d, out.data_ptr(), DTYPES[out.dtype], ld,
+                                     _stream(stream)), "gift_act_restore")
+        return out
+
+
+def norm_forward(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, kind="layer", ckpt=None, out=None,
+                 stream=None):
+    """Layer norm (kind "layer") or RMS norm ("rms") of the rows of x [T][d]:
+    returns y (of x's type), mean (None for "rms") and rstd, fp32 [T].  With
+    `ckpt` (an ActCheckpoint of the same T and d) x is also saved there.
+    weight and bias: of x's type or both fp32."""
+    kind = NORMS.get(kind, kind)
+    ld = _rows(x, "x")
+    (T, d), dev = x.shape, x.device
+    wt = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
+    _vector(weight, "weight", d, (x.dtype, torch.float32), dev)
+    _vector(bias, "bias", d, (wt,), dev)
+    if ckpt is not None and (ckpt.T, ckpt.d) != (T, d):
+        raise ValueError("the checkpoint has another shape than x")
+    y = _empty(stream, (T, d), x.dtype, dev) if out is None else out
+    ldy = _rows(y, "out", T, d, x.dtype)
+    mean = _empty(stream, (T,), torch.float32, dev) if kind == NORM_LAYER else None
+    rstd = _empty(stream, (T,), torch.float32, dev)
+    _check(_lib.gift_norm_forward(kind, x.data_ptr(), DTYPES[x.dtype], ld, T, d, _ptr(weight), _ptr(bias), DTYPES[wt],
+                                  eps, y.data_ptr(), ldy, _ptr(mean), rstd.data_ptr(),
+                                  None if ckpt is None else ckpt._ref, _stream(stream)), "gift_norm_forward")
+    return y, mean, rstd
+
+
+def norm_backward(dy: torch.Tensor, x, mean, rstd, weight=None, kind="layer", dx=None, dweight=None, dbias=None,
+                  accumulate: bool = False, work=None, stream=None):
+    """Backward of norm_forward.  x: the forward's input, or its ActCheckpoint.
+    Returns dx (of dy's type), dweight and dbias (fp32 [d]; dbias None for
+    "rms" unless given).  accumulate: added to the given dweight and dbias."""
+    kind = NORMS.get(kind, kind)
+    ld = _rows(dy, "dy")
+    (T, d), dev = dy.shape, dy.device
+    ck = x if isinstance(x, ActCheckpoint) else None
+    if ck is not None:
+        if (ck.T, ck.d) != (T, d):
+            raise ValueError("the checkpoint has another shape than dy")
+        ldx, xp = 0, None
+    else:
+        ldx, xp = _rows(x, "x", T, d, dy.dtype), x.data_ptr()
+    _vector(weight, "weight", d, (dy.dtype, torch.float32), dev)
+    _vector(mean, "mean", T, (torch.float32,), dev)
+    _vector(rstd, "rstd", T, (torch.float32,), dev)
+    if accumulate and dweight is None and dbias is None:
+        raise ValueError("accumulate needs the gradients to add to")
+    if not accumulate:
+        if dweight is None:
+            dweight = _empty(stream, (d,), torch.float32, dev)
+        if dbias is None and kind == NORM_LAYER:
+            dbias = _empty(stream, (d,), torch.float32, dev)
+    _vector(dweight, "dweight", d, (torch.float32,), dev)
+    _vector(dbias, "dbias", d, (torch.float32,), dev)
+    if dx is None:
+        dx = _empty(stream, (T, d), dy.dtype, dev)
+    lddx = _rows(dx, "dx", T, d, dy.dtype)
+    if work is None:
+        work = _empty(stream, (int(_lib.gift_norm_workspace_bytes(T, d)),), torch.uint8, dev)
+    wt = dy.dtype if weight is None else weight.dtype
+    _check(_lib.gift_norm_backward(kind, dy.data_ptr(), DTYPES[dy.dtype], ld, xp, ldx, None if ck is None else ck._ref,
+                                   T, d, _ptr(weight), DTYPES[wt], _ptr(mean), _ptr(rstd), dx.data_ptr(), lddx,
+                                   _ptr(dweight), _ptr(dbias), int(accumulate), work.data_ptr(), work.numel(),
+                                   _stream(stream)), "gift_norm_backward")
+    return dx, dweight, dbias
+
+
+def weight_grad(delta: torch.Tensor, ckpt: ActCheckpoint, alpha: float = 1.0, out=None, accumulate: bool = False,
+                work=None, stream=None) -> torch.Tensor:
+    """alpha delta^T a [m][d] in fp32 (plus `out` when accumulate), from the
+    output gradients delta [T][m] and the checkpoint of the layer's input a
+    [T][d]: the gradient Layer.encode takes."""
+    T, d = ckpt.T, ckpt.d
+    ld = _rows(delta, "delta", T)
+    m, dev = delta.shape[1], delta.device
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs the tensor to add to")
+        out = _empty(stream, (m, d), torch.float32, dev)
+    ldw = _rows(out, "out", m, d, torch.float32)
+    dt = DTYPES[delta.dtype]
+    if work is None:
+        work = _empty(stream, (int(_lib.gift_weight_grad_workspace_bytes(T, m, d, dt)),), torch.uint8, dev)
+    _check(_lib.gift_weight_grad(delta.data_ptr(), dt, ld, m, ckpt._ref, T, d, alpha, int(accumulate), out.data_ptr(),
+                                 ldw, work.data_ptr(), work.numel(), _stream(stream)), "gift_weight_grad")
+    return out

@@ -173,6 +173,8 @@ namespace gift {
 
 int max_resident_cap() { return g_max_resident; }
 
+gift_status hip_failure(hipError_t e) { return hip_fail(e); }
+
 // Device-wide order of the persistent launches.  Two persistent kernels
 // that shared the device could each hold part of it while waiting for their
 // own workgroups that have no room to start.  Launches on one stream are

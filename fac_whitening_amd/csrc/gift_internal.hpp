@@ -242,6 +242,50 @@ hipError_t launch_trmm(const float* x, int64_t ldx, int m, int d, const float* M
 // local per-tensor amax (already in slot).
 hipError_t launch_hits(const float* g, int64_t n, int fmt, const uint32_t* slot,
                        unsigned long long* counts, hipStream_t s);
+// Activation operators (k_act.hip, k_norm.hip, k_wgrad.hip).
+constexpr int kNormMaxCols = 16384;
+// Keeps the HIP error for gift_last_hip_error; returns GIFT_ERR_HIP.
+gift_status hip_failure(hipError_t e);
+struct NormCall {
+  int kind, dtype, wdtype;
+  const void* x;
+  int64_t ldx;
+  const gift_act_ckpt* ckpt;
+  int64_t T;
+  int d;
+  const void *w, *b;
+  float eps;
+  float *mean, *rstd;
+  void* y;              // forward: y; backward: dx
+  int64_t ldy;
+  const void* dy;
+  int64_t lddy;
+};
+struct WgradCall {
+  const void* delta;
+  int dtype;
+  int64_t ldd;
+  int m;
+  const gift_act_ckpt* ckpt;
+  int64_t T;
+  int d;
+  float alpha;
+  int accumulate;
+  float* W;
+  int64_t ldw;
+};
+int64_t act_grid(int64_t T, int d);
+hipError_t launch_act_save(const void* x, int dtype, int64_t ld, int64_t T, int d, const gift_act_ckpt& c,
+                           hipStream_t s);
+hipError_t launch_act_restore(const gift_act_ckpt& c, int64_t T, int d, void* out, int dtype, int64_t ld,
+                              hipStream_t s);
+// Partial sums (rows of [2][d] fp32) of the norm backward's parameter gradients.
+int norm_partials(int64_t T, int d);
+int64_t norm_forward_grid(int64_t T, int d);
+hipError_t launch_norm_forward(const NormCall& c, hipStream_t s);
+hipError_t launch_norm_backward(const NormCall& c, float* part, float* dw, float* db, int accumulate, hipStream_t s);
+hipError_t launch_weight_grad(const WgradCall& c, hipStream_t s);
+
 hipError_t launch_amax_out(const uint32_t* slots, float* amax_out, int64_t n, hipStream_t s);
 hipError_t launch_amax_flat(const float* g, int64_t n, uint32_t* slot, hipStream_t s);
 

@@ -1,0 +1,488 @@
+// Layer norm and RMS norm over rows: forward (optionally keeping its input as
+// an 8-bit checkpoint in the same pass) and backward, from the input or from
+// its checkpoint, with the reduction of the weight's and bias's gradients.
+//
+// GIFT 阅读笔记, §实验设置: the layers whose gradients the codec carries are
+// the MLP layers of Llama-class models; a norm stands in front of each block
+// of them.
+//
+//   mean = sum_j x_j / d (0 for RMS),  rstd = (sum_j (x_j - mean)^2 / d + eps)^-1/2
+//   xh = (x - mean) rstd,              y = xh gamma + beta
+//   g = dy gamma,  c1 = sum_j g_j xh_j / d,  c2 = sum_j g_j / d (0 for RMS)
+//   dx = rstd (g - c2 - xh c1),  dgamma = sum_t dy xh,  dbeta = sum_t dy
+//
+// Everything is computed in fp32; y and dx are rounded once to the element
+// type.  The variance is the sum of squares about the mean (the row is in
+// registers, so the second pass costs no memory traffic and does not cancel).
+//
+// Both are bound by memory.  A row is held by G lanes, 8 elements (one
+// 16-byte load of a 16-bit type) per lane and chunk, CH chunks: G = 16 for
+// d <= 128, a wave up to 2048, a workgroup of 256 up to 8192 and of 512 up to
+// 16384 columns.  Sums inside 64 lanes are lane exchanges; wider groups add
+// their waves' sums through LDS.
+#include <type_traits>
+
+#include "act8.hpp"
+
+namespace gift {
+
+struct NormArgs {
+  const void* x;
+  int64_t ldx;
+  uint8_t* codes;       // checkpoint: written by the forward, read by the backward (NULL: none)
+  int64_t ldc;
+  uint8_t* bscales;
+  int nb, fmt;
+  const void *w, *b;    // gamma, beta (NULL: ones, zeros)
+  int w32;              // gamma, beta in fp32 (otherwise in the element type)
+  int layer;            // 1: layer norm, 0: RMS norm
+  int64_t T;
+  int d;
+  float eps, invd;
+  float *mean, *rstd;   // forward: written (either may be NULL); backward: read
+  void* y;              // forward: y; backward: dx
+  int64_t ldy;
+  const void* dy;
+  int64_t lddy;
+  float* part;          // backward: [P][2][d] partial sums of dgamma, dbeta (NULL: not wanted)
+  int64_t groups;       // backward: row groups (kNormRows<G> rows each)
+};
+
+namespace {
+
+template <int G>
+constexpr int kNormThreads = G > 256 ? G : 256;
+// Rows per step of a workgroup, and per group of 8 (16 for G = 16) rows whose
+// exponents share cache lines.
+template <int G>
+constexpr int kNormRows = G == 16 ? 16 : 8;
+
+// Sums of N values over the G lanes of a row.  Groups wider than a wave pass
+// through `red` (two buffers in turn, so one barrier per call is enough).
+template <int G, int N>
+__device__ __forceinline__ void row_sums(float* v, float (*red)[2][8], int& flip) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = lanes_sum<G == 16 ? 16 : 64>(v[i]);
+  if constexpr (G > 64) {
+    constexpr int W = G / 64;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[flip][i][wave] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = red[flip][i][0];
+#pragma unroll
+      for (int k = 1; k < W; ++k) s += red[flip][i][k];
+      v[i] = s;
+    }
+    flip ^= 1;
+  }
+}
+
+// Eight weights at column col (n of them inside the row).
+template <typename T>
+__device__ __forceinline__ void load_weights(const void* p, int w32, int col, int n, float* v) {
+  if (w32) unpack8(load8(static_cast<const float*>(p) + col, n), v);
+  else unpack8(load8(static_cast<const T*>(p) + col, n), v);
+}
+
+// Raw chunk c of the row at t: the elements, or the codes and the exponent
+// of the chunk's block.
+template <typename T, bool CK>
+struct RowChunk {
+  Raw8<T> r;
+};
+template <typename T>
+struct RowChunk<T, true> {
+  uint32_t w[2];
+  uint32_t e;
+};
+
+template <typename T>
+__device__ __forceinline__ void load_chunk(RowChunk<T, false>& c, const NormArgs& a, int64_t t, int col, int n) {
+  c.r = load8(static_cast<const T*>(a.x) + t * a.ldx + col, n);
+}
+template <typename T>
+__device__ __forceinline__ void load_chunk(RowChunk<T, true>& c, const NormArgs& a, int64_t t, int col, int n) {
+  c.w[0] = c.w[1] = 0;
+  c.e = kActExpMin;
+  if (n > 0) {
+    __builtin_memcpy(c.w, __builtin_assume_aligned(a.codes + t * a.ldc + col, 8), 8);
+    c.e = a.bscales[((t >> 3) * a.nb + col / kActBlock) * kActGroup + (t & 7)];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void chunk_values(const RowChunk<T, false>& c, const NormArgs&, float* v) {
+  unpack8(c.r, v);
+}
+template <typename T>
+__device__ __forceinline__ void chunk_values(const RowChunk<T, true>& c, const NormArgs& a, float* v) {
+  act_decode8(c.w, c.e, a.fmt, v);
+}
+
+}  // namespace
+
+// Forward.  R rows per group of lanes at once (their loads are in flight
+// together); a workgroup covers 8 rows (16 for G = 16), or one row when G is
+// the whole workgroup.  In that last case consecutive workgroups go to
+// different dies (round robin over 8); the row map below gives the 8 rows of
+// one exponent group to one die, so their bytes merge in one L2.
+template <typename T, int G, int CH>
+__global__ void __launch_bounds__(kNormThreads<G>) k_norm_fwd(NormArgs a) {
+  constexpr int NT = kNormThreads<G>;
+  constexpr int S = NT / G;                                 // rows of a step
+  constexpr int R = G > 64 ? 1 : kNormRows<G> / S;          // rows per lane group
+  __shared__ float red[2][2][8];
+  int flip = 0;
+  const int lane = threadIdx.x % G, sub = threadIdx.x / G;
+  int64_t row0;
+  if constexpr (G > 64) {
+    const int64_t b = blockIdx.x;
+    row0 = (b & ~(int64_t)63) + (b & 7) * 8 + ((b >> 3) & 7);
+    if (row0 >= a.T) return;
+  } else {
+    row0 = (int64_t)blockIdx.x * kNormRows<G> + sub * R;
+    if (row0 >= a.T) return;   // per wave or part of a wave; no barriers below for these G
+  }
+  Raw8<T> raw[R][CH];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (c * G + lane) * 8;
+      raw[r][c] = load8(static_cast<const T*>(a.x) + (row0 + r) * a.ldx + col, row0 + r < a.T ? a.d - col : 0);
+    }
+  float mean[R], rstd[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    mean[r] = 0.f;
+    if (a.layer) {
+      float s = 0.f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float v[8];
+        unpack8(raw[r][c], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += v[j];
+      }
+      row_sums<G, 1>(&s, red, flip);
+      mean[r] = s / (float)a.d;   // correctly rounded: a constant row is centred exactly
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int n = a.d - (c * G + lane) * 8;
+      float v[8];
+      unpack8(raw[r][c], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = j < n ? v[j] - mean[r] : 0.f;
+        q += u * u;
+      }
+    }
+    row_sums<G, 1>(&q, red, flip);
+    rstd[r] = 1.0f / sqrtf(q / (float)a.d + a.eps);
+    if (lane == 0 && row0 + r < a.T) {
+      if (a.mean) a.mean[row0 + r] = mean[r];
+      if (a.rstd) a.rstd[row0 + r] = rstd[r];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = (c * G + lane) * 8;
+    const int n = a.d - col;
+    float w[8], b[8];
+    if (a.w) load_weights<T>(a.w, a.w32, col, n, w);
+    if (a.b) load_weights<T>(a.b, a.w32, col, n, b);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t t = row0 + r;
+      float v[8], y[8];
+      unpack8(raw[r][c], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        y[j] = (v[j] - mean[r]) * rstd[r];
+        if (a.w) y[j] *= w[j];
+        if (a.b) y[j] += b[j];
+      }
+      Raw8<T> o;
+      pack8(y, o);
+      if (t < a.T) store8(static_cast<T*>(a.y) + t * a.ldy + col, o, n);
+      if (a.codes) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t u = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+          m = u > m ? u : m;
+        }
+        const uint32_t e = act_exponent(quad_max(m), a.fmt);
+        uint32_t k[2];
+        act_encode8(v, e, a.fmt, k);
+        if (t < a.T && col < a.nb * kActBlock) {
+          __builtin_memcpy(__builtin_assume_aligned(a.codes + t * a.ldc + col, 8), k, 8);
+          if ((lane & 3) == 0)
+            a.bscales[((t >> 3) * a.nb + col / kActBlock) * kActGroup + (t & 7)] = (uint8_t)e;
+        }
+      }
+    }
+  }
+}
+
+// Backward.  Workgroup p takes the row groups p, p + P, ...; each lane keeps
+// the dgamma and dbeta sums of its own columns in registers over all of them
+// and fetches the next row while it works on the present one.  The partial
+// sums of the workgroups go to part [P][2][d] and are added in order by
+// k_norm_reduce: no atomics, the same result every time.
+template <typename T, bool CK, int G, int CH>
+__global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
+  constexpr int NT = kNormThreads<G>;
+  constexpr int S = NT / G, RB = kNormRows<G>, STEPS = RB / S;
+  __shared__ float red[2][2][8];
+  __shared__ float comb[S > 1 ? S : 1][S > 1 ? G : 1][9];   // padded: 9 words a lane, no bank conflicts
+  int flip = 0;
+  const int lane = threadIdx.x % G, sub = threadIdx.x / G;
+  // Above 12288 columns neither the next row nor the weights fit the
+  // registers (256 a lane at 512 threads): there a row is fetched when its
+  // turn comes, and the weights come from the cache each time.
+  constexpr bool AHEAD = !(G == 512 && CH == 4);
+  float wk[AHEAD ? CH : 1][8], dg[CH][8], db[CH][8];
+  auto weights = [&](int c, float* v) {
+    const int col = (c * G + lane) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 1.f;
+    if (a.w) load_weights<T>(a.w, a.w32, col, a.d - col, v);
+  };
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[c][j] = db[c][j] = 0.f;
+    if constexpr (AHEAD) weights(c, wk[c]);
+  }
+  RowChunk<T, CK> xr[CH];
+  Raw8<T> yr[CH];
+  float mean_n = 0.f, rstd_n = 0.f;
+  // step k of this workgroup: row group p + (k / STEPS) P, its rows k % STEPS
+  const int64_t mine = a.groups > blockIdx.x ? cdiv(a.groups - blockIdx.x, gridDim.x) : 0;
+  const int64_t steps = mine * STEPS;
+  auto row_of = [&](int64_t k) {
+    return ((int64_t)blockIdx.x + (k / STEPS) * gridDim.x) * RB + (k % STEPS) * S + sub;
+  };
+  auto fetch = [&](int64_t k) {
+    const int64_t t = row_of(k);
+    const bool in = k < steps && t < a.T;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (c * G + lane) * 8;
+      load_chunk(xr[c], a, t, col, in ? a.d - col : 0);
+      yr[c] = load8(static_cast<const T*>(a.dy) + t * a.lddy + col, in ? a.d - col : 0);
+    }
+    mean_n = in && a.layer ? a.mean[t] : 0.f;
+    rstd_n = in ? a.rstd[t] : 0.f;
+  };
+  if (AHEAD) fetch(0);
+  for (int64_t k = 0; k < steps; ++k) {
+    const int64_t t = row_of(k);
+    if (!AHEAD) fetch(k);
+    const float mean = mean_n, rstd = rstd_n;
+    float xh[CH][8], t8[CH][8];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int n = t < a.T ? a.d - (c * G + lane) * 8 : 0;
+      float* w = wk[AHEAD ? c : 0];
+      if constexpr (!AHEAD) weights(c, w);
+      chunk_values(xr[c], a, xh[c]);
+      unpack8(yr[c], t8[c]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // columns past the row (and rows past T) add nothing: dy reads zero there
+        xh[c][j] = j < n ? (xh[c][j] - mean) * rstd : 0.f;
+        const float g = t8[c][j] * w[j];
+        s[0] += g * xh[c][j];
+        s[1] += g;
+        dg[c][j] += t8[c][j] * xh[c][j];
+        db[c][j] += t8[c][j];
+      }
+    }
+    if (AHEAD) fetch(k + 1);
+    row_sums<G, 2>(s, red, flip);
+    const float c1 = s[0] * a.invd, c2 = a.layer ? s[1] * a.invd : 0.f;
+    if (t < a.T) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = (c * G + lane) * 8;
+        float* w = wk[AHEAD ? c : 0];
+        if constexpr (!AHEAD) weights(c, w);
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = rstd * (t8[c][j] * w[j] - c2 - xh[c][j] * c1);
+        Raw8<T> r;
+        pack8(o, r);
+        store8(static_cast<T*>(a.y) + t * a.ldy + col, r, a.d - col);
+      }
+    }
+  }
+  if (!a.part) return;
+  // this workgroup's sums: the S row slots are added through LDS in order
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float* v = which == 0 ? dg[c] : db[c];
+      const int col = (c * G + lane) * 8;
+      if constexpr (S > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) comb[sub][lane][j] = v[j];
+        __syncthreads();
+        if (sub != 0) continue;
+#pragma unroll
+        for (int q = 1; q < S; ++q)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += comb[q][lane][j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j < a.d) part[(int64_t)which * a.d + col + j] = v[j];
+    }
+}
+
+// dgamma, dbeta [d] from part [P][2][d]: a workgroup adds 64 columns (32
+// threads down the partials for each), four sums in turn per thread, then
+// the threads' sums in order.  accumulate: added to what the outputs hold.
+constexpr int kReduceCols = 32, kReduceRows = 32;
+__global__ void __launch_bounds__(kReduceCols* kReduceRows) k_norm_reduce(const float* __restrict__ part, int P, int d,
+                                                                         float* __restrict__ dw, float* __restrict__ db,
+                                                                         int accumulate) {
+  __shared__ float sums[kReduceRows][kReduceCols + 1];
+  const int cx = threadIdx.x % kReduceCols, ry = threadIdx.x / kReduceCols;
+  const int j = blockIdx.x * kReduceCols + cx;   // column of [2][d]
+  float v = 0.f;
+  if (j < 2 * d)
+    for (int p = ry; p < P; p += kReduceRows) v += part[(int64_t)p * 2 * d + j];
+  sums[ry][cx] = v;
+  __syncthreads();
+  if (ry != 0 || j >= 2 * d) return;
+#pragma unroll
+  for (int q = 1; q < kReduceRows; ++q) v += sums[q][cx];
+  float* out = j < d ? (dw ? dw + j : nullptr) : (db ? db + (j - d) : nullptr);
+  if (out) *out = accumulate ? *out + v : v;
+}
+
+namespace {
+
+// Calls f with the lane group and chunk count for d columns.
+template <typename F>
+void norm_variant(int d, F&& f) {
+  using std::integral_constant;
+  const integral_constant<int, 64> wave;
+  const integral_constant<int, 256> four;
+  const integral_constant<int, 512> eight;
+  if (d <= 128) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (d <= 512) f(wave, integral_constant<int, 1>{});
+  else if (d <= 1024) f(wave, integral_constant<int, 2>{});
+  else if (d <= 1536) f(wave, integral_constant<int, 3>{});
+  else if (d <= 2048) f(wave, integral_constant<int, 4>{});
+  else if (d <= 4096) f(four, integral_constant<int, 2>{});
+  else if (d <= 6144) f(four, integral_constant<int, 3>{});
+  else if (d <= 8192) f(four, integral_constant<int, 4>{});
+  else if (d <= 12288) f(eight, integral_constant<int, 3>{});
+  else f(eight, integral_constant<int, 4>{});
+}
+
+}  // namespace
+
+int64_t norm_row_groups(int64_t T, int d) { return cdiv(T, d <= 128 ? 16 : 8); }
+
+// Workgroups of the backward pass: at most 512, two a compute unit (their partial
+// sums cost 16 d bytes each), never more than there are row groups.
+int norm_partials(int64_t T, int d) {
+  const int64_t g = norm_row_groups(T, d);
+  return (int)(g < 512 ? (g > 0 ? g : 1) : 512);
+}
+
+static NormArgs norm_args(const NormCall& c) {
+  NormArgs a{};
+  a.x = c.x;
+  a.ldx = c.ldx;
+  if (c.ckpt) {
+    a.codes = c.ckpt->d_codes;
+    a.ldc = c.ckpt->ldc;
+    a.bscales = c.ckpt->d_bscales;
+    a.fmt = c.ckpt->fmt;
+  }
+  a.nb = (int)cdiv(c.d, kActBlock);
+  a.w = c.w;
+  a.b = c.b;
+  a.w32 = c.wdtype == GIFT_FP32;
+  a.layer = c.kind == GIFT_NORM_LAYER;
+  a.T = c.T;
+  a.d = c.d;
+  a.eps = c.eps;
+  a.invd = (float)(1.0 / c.d);
+  a.mean = c.mean;
+  a.rstd = c.rstd;
+  a.y = c.y;
+  a.ldy = c.ldy;
+  a.dy = c.dy;
+  a.lddy = c.lddy;
+  return a;
+}
+
+// Workgroups of the forward: a row each above 2048 columns (whole sets of 64
+// for the row map), a row group each below.
+int64_t norm_forward_grid(int64_t T, int d) { return d > 2048 ? cdiv(T, 64) * 64 : norm_row_groups(T, d); }
+
+template <typename T>
+static void norm_fwd_t(const NormArgs& a, hipStream_t s) {
+  norm_variant(a.d, [&](auto g, auto ch) {
+    constexpr int G = decltype(g)::value, CH = decltype(ch)::value;
+    hipLaunchKernelGGL((k_norm_fwd<T, G, CH>), dim3((unsigned)norm_forward_grid(a.T, a.d)),
+                       dim3(kNormThreads<G>), 0, s, a);
+  });
+}
+
+hipError_t launch_norm_forward(const NormCall& c, hipStream_t s) {
+  if (c.T == 0) return hipSuccess;
+  const NormArgs a = norm_args(c);
+  if (c.dtype == GIFT_BF16) norm_fwd_t<Bf16>(a, s);
+  else if (c.dtype == GIFT_FP16) norm_fwd_t<Fp16>(a, s);
+  else norm_fwd_t<float>(a, s);
+  return hipGetLastError();
+}
+
+template <typename T, bool CK>
+static void norm_bwd_t(const NormArgs& a, int P, hipStream_t s) {
+  norm_variant(a.d, [&](auto g, auto ch) {
+    constexpr int G = decltype(g)::value, CH = decltype(ch)::value;
+    hipLaunchKernelGGL((k_norm_bwd<T, CK, G, CH>), dim3((unsigned)P), dim3(kNormThreads<G>), 0, s, a);
+  });
+}
+
+hipError_t launch_norm_backward(const NormCall& c, float* part, float* dw, float* db, int accumulate, hipStream_t s) {
+  const int P = norm_partials(c.T, c.d);
+  NormArgs a = norm_args(c);
+  a.part = part;
+  a.groups = norm_row_groups(c.T, c.d);
+  if (c.ckpt) {
+    if (c.dtype == GIFT_BF16) norm_bwd_t<Bf16, true>(a, P, s);
+    else if (c.dtype == GIFT_FP16) norm_bwd_t<Fp16, true>(a, P, s);
+    else norm_bwd_t<float, true>(a, P, s);
+  } else {
+    if (c.dtype == GIFT_BF16) norm_bwd_t<Bf16, false>(a, P, s);
+    else if (c.dtype == GIFT_FP16) norm_bwd_t<Fp16, false>(a, P, s);
+    else norm_bwd_t<float, false>(a, P, s);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (part)
+    hipLaunchKernelGGL(k_norm_reduce, dim3((unsigned)cdiv(2 * (int64_t)c.d, kReduceCols)),
+                       dim3(kReduceCols * kReduceRows), 0, s, part, P, c.d, dw, db, accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace gift

@@ -74,7 +74,7 @@ enum gift_scaling {
   GIFT_SCALE_BLOCK16 = 2,
   GIFT_SCALE_BLOCK512 = 3
 };
-enum gift_dtype { GIFT_BF16 = 0, GIFT_FP32 = 1 };
+enum gift_dtype { GIFT_BF16 = 0, GIFT_FP32 = 1, GIFT_FP16 = 2 /* activation operators only */ };
 enum gift_side { GIFT_SIDE_A = 0, GIFT_SIDE_G = 1 };      /* input / output statistics */
 enum { GIFT_FLAG_NONFINITE = 1u, GIFT_FLAG_SPIN_TIMEOUT = 2u };
 
@@ -403,6 +403,88 @@ gift_status gift_group_create(int32_t n, const gift_group_item* items, int32_t R
 gift_status gift_group_destroy(gift_group_t group);
 gift_status gift_group_encode(gift_group_t group, gift_stream_t stream);
 gift_status gift_group_decode_reduce(gift_group_t group, gift_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Activation operators: what surrounds a layer whose gradient is encoded.
+ * [Note] §前置知识 Eq. (4): the backward pass forms W_g = delta^T a from the
+ * layer's input a; §实验设置: Llama-class MLP layers, a norm before each.
+ *
+ *   gift_act_save / gift_act_restore   8-bit checkpoint of an activation
+ *   gift_norm_forward / _backward      layer norm and RMS norm; the forward can keep its input as a
+ *                                      checkpoint, the backward can read it instead of the input
+ *   gift_weight_grad                   W = alpha delta^T a from the checkpoint of a, fp32: gift_encode's input
+ *
+ * They are stateless (no handle) and may be called from any thread.  Element
+ * types are GIFT_BF16, GIFT_FP16 and GIFT_FP32.  Unlike the calls above, rows
+ * of elements may start anywhere: pointers need the alignment of their
+ * element type only, and a leading dimension is any number >= the row length
+ * (16-byte aligned rows are the fastest).  T = 0 is valid everywhere.
+ * Non-finite elements give what IEEE arithmetic gives; there is no flag.
+ * All results are the same on every call (no atomics) and every call may be
+ * captured into a graph.
+ *
+ * A checkpoint of x [T][d] is caller-owned device memory in two arrays:
+ *   d_codes    uint8 [T][ldc], ldc a multiple of 32, >= d; 16-byte aligned.
+ *              FP8 codes (GIFT_E4M3 or GIFT_E5M2); saving writes columns
+ *              0 .. 32 ceil(d / 32) - 1 (zero codes past d).
+ *   d_bscales  uint8, gift_act_scale_bytes(T, d) bytes, 16-byte aligned: one
+ *              biased exponent e per token t and 32-column block b at
+ *              [t / 8][b][t % 8] of [ceil(T / 8)][ceil(d / 32)][8].
+ * e is the smallest integer >= 32 with amax <= FMAX 2^(e - 127) over the
+ * block (FMAX 448 or 57344: nothing saturates); code = x 2^(127 - e) rounded to
+ * nearest even, value = code 2^(e - 127).  A block that holds an Inf or NaN
+ * has e = 255 and codes 0x7F: all its values are NaN.  Exponents in memory
+ * that a save did not write must be in 32..247 or 255.
+ * ------------------------------------------------------------------------- */
+typedef struct gift_act_ckpt {
+  uint8_t* d_codes;
+  int64_t ldc;
+  uint8_t* d_bscales;
+  int32_t fmt;              /* GIFT_E4M3 or GIFT_E5M2 */
+} gift_act_ckpt;
+size_t gift_act_scale_bytes(int64_t T, int32_t d);   /* 0 for invalid sizes */
+/* d_x [T][ldx] -> checkpoint. */
+gift_status gift_act_save(const void* d_x, int32_t dtype, int64_t ldx, int64_t T, int32_t d,
+                          const gift_act_ckpt* h_ckpt, gift_stream_t stream);
+/* checkpoint -> d_out [T][ldo] (bf16 and fp32 hold every value exactly; fp16 rounds to nearest even). */
+gift_status gift_act_restore(const gift_act_ckpt* h_ckpt, int64_t T, int32_t d, void* d_out, int32_t dtype,
+                             int64_t ldo, gift_stream_t stream);
+
+/* Row norms over d columns, 1 <= d <= 16384 (GIFT_ERR_UNSUPPORTED beyond):
+ *   mean = sum x / d (0 for GIFT_NORM_RMS), rstd = (sum (x - mean)^2 / d + eps)^-1/2
+ *   y = (x - mean) rstd gamma + beta
+ * in fp32, y rounded once to `dtype`, the type of x, y, dy and dx.  gamma and
+ * beta [d] are of type wdtype (`dtype` or GIFT_FP32); NULL: ones, zeros. */
+enum gift_norm { GIFT_NORM_LAYER = 0, GIFT_NORM_RMS = 1 };
+/* d_mean, d_rstd: fp32 [T] outputs for the backward pass, either may be NULL.
+ * h_ckpt: also save x there (NULL: do not).  d_y may be d_x. */
+gift_status gift_norm_forward(int32_t kind, const void* d_x, int32_t dtype, int64_t ldx, int64_t T, int32_t d,
+                              const void* d_gamma, const void* d_beta, int32_t wdtype, float eps, void* d_y,
+                              int64_t ldy, float* d_mean, float* d_rstd, const gift_act_ckpt* h_ckpt,
+                              gift_stream_t stream);
+/* Workspace of gift_norm_backward when a weight or bias gradient is wanted. */
+size_t gift_norm_workspace_bytes(int64_t T, int32_t d);
+/* With xh = (x - mean) rstd, g = dy gamma:
+ *   dx = rstd (g - sum g / d [layer norm only] - xh sum (g xh) / d)
+ *   dgamma = sum_t dy xh, dbeta = sum_t dy     (fp32 [d], either may be NULL; accumulate != 0 adds to
+ *                                               what they hold, for micro-batches)
+ * x comes from d_x or, when that is NULL, from the checkpoint h_ckpt (one
+ * of the two is given, not both).  d_mean (layer norm only) and d_rstd are the forward's.  d_dx may be
+ * d_dy or d_x.  d_work: 16-byte aligned (NULL when no parameter gradient is asked for). */
+gift_status gift_norm_backward(int32_t kind, const void* d_dy, int32_t dtype, int64_t lddy, const void* d_x,
+                               int64_t ldx, const gift_act_ckpt* h_ckpt, int64_t T, int32_t d, const void* d_gamma,
+                               int32_t wdtype, const float* d_mean, const float* d_rstd, void* d_dx, int64_t lddx,
+                               float* d_dgamma, float* d_dbeta, int32_t accumulate, void* d_work, size_t work_bytes,
+                               gift_stream_t stream);
+
+/* W [m][ldw] = alpha delta^T a (+ W when accumulate != 0), delta [T][ldd] of
+ * type `dtype`, a [T][d] the values of the checkpoint.  delta enters the products
+ * without loss (an fp32 value as the sum of three bf16 numbers, an fp16 value of two), a is
+ * exact in bf16, sums are fp32. */
+size_t gift_weight_grad_workspace_bytes(int64_t T, int32_t m, int32_t d, int32_t dtype);
+gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, int32_t m, const gift_act_ckpt* h_ckpt,
+                             int64_t T, int32_t d, float alpha, int32_t accumulate, float* d_W, int64_t ldw,
+                             void* d_work, size_t work_bytes, gift_stream_t stream);
 
 /* Scale-sync schedule ([Note] Algorithm 1, its scale-sync step): the geometry-aware
  * layers quantise with their local scale and, on a scale-sync step, with the
