@@ -138,7 +138,7 @@ gift_status gift_norm_backward(int32_t kind, const void* d_dy, int32_t dtype, in
 
 size_t gift_weight_grad_workspace_bytes(int64_t T, int32_t m, int32_t d, int32_t dtype) {
   if (!sizes_ok(T, d) || m < 1 || m > kMaxCols || !dtype_ok(dtype)) return 0;
-  return 256;
+  return gift::wgrad_workspace(T, m, d, dtype);
 }
 
 gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, int32_t m, const gift_act_ckpt* h_ckpt,
@@ -147,6 +147,8 @@ gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, in
   if (!dtype_ok(dtype) || !sizes_ok(T, d) || m < 1 || m > kMaxCols) return GIFT_ERR_INVALID_ARG;
   if (!rows_ok(d_delta, dtype, ldd, T, m) || !ckpt_ok(h_ckpt, T, d)) return GIFT_ERR_INVALID_ARG;
   if (!d_W || !aligned(d_W, 4) || ldw < d) return GIFT_ERR_INVALID_ARG;
+  if (!d_work || !aligned(d_work, 16)) return GIFT_ERR_INVALID_ARG;
+  if (work_bytes < gift_weight_grad_workspace_bytes(T, m, d, dtype)) return GIFT_ERR_WORKSPACE;
   gift::WgradCall c{};
   c.delta = d_delta;
   c.dtype = dtype;
@@ -159,6 +161,7 @@ gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, in
   c.accumulate = accumulate ? 1 : 0;
   c.W = d_W;
   c.ldw = ldw;
+  c.work = static_cast<float*>(d_work);
   return result(gift::launch_weight_grad(c, static_cast<hipStream_t>(stream)));
 }
 

@@ -273,6 +273,7 @@ struct WgradCall {
   int accumulate;
   float* W;
   int64_t ldw;
+  float* work;          // wgrad_workspace bytes
 };
 int64_t act_grid(int64_t T, int d);
 hipError_t launch_act_save(const void* x, int dtype, int64_t ld, int64_t T, int d, const gift_act_ckpt& c,
@@ -284,6 +285,7 @@ int norm_partials(int64_t T, int d);
 int64_t norm_forward_grid(int64_t T, int d);
 hipError_t launch_norm_forward(const NormCall& c, hipStream_t s);
 hipError_t launch_norm_backward(const NormCall& c, float* part, float* dw, float* db, int accumulate, hipStream_t s);
+size_t wgrad_workspace(int64_t T, int m, int d, int dtype);
 hipError_t launch_weight_grad(const WgradCall& c, hipStream_t s);
 
 hipError_t launch_amax_out(const uint32_t* slots, float* amax_out, int64_t n, hipStream_t s);

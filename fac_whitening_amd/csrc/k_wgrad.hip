@@ -5,6 +5,8 @@
 //
 // GIFT 阅读笔记, §前置知识 Eq. (4) and §核心想法: W_g = delta^T a of a linear
 // layer, averaged over the tokens (alpha = 1 / T).
+#include <type_traits>
+
 #include "act8.hpp"
 
 namespace gift {
@@ -22,11 +24,475 @@ struct WgradArgs {
   int accumulate;
   float* W;
   int64_t ldw;
+  float* part;             // segments of tiles split over workgroups
+  int nst;                 // token stages of a tile
+  int nbm, nbn;            // output tiles down and across
+  int rounds;              // whole tiles of each workgroup
 };
 
 __device__ __forceinline__ float elem_f32(const float* p) { return *p; }
 __device__ __forceinline__ float elem_f32(const Bf16* p) { return __uint_as_float((uint32_t)p->v << 16); }
 __device__ __forceinline__ float elem_f32(const Fp16* p) { return (float)__builtin_bit_cast(_Float16, p->v); }
+
+// ---------------------------------------------------------------------------
+// Matrix-core form.  One workgroup (4 waves, 2 x 2) per output tile of 64 MT x
+// 64 NT, KT tokens a stage.
+//  * Products are v_mfma_f32_32x32x16_bf16.  A checkpoint value is exact in
+//    bf16; delta enters as P bf16 planes whose sum is delta: bf16 itself, fp16
+//    (11 bits) as two, fp32 (24 bits) as three, each the leading 8 bits of
+//    what the planes before it leave (truncation: no plane overflows, the
+//    remainders are exact).  Products are exact in fp32, sums are fp32.
+//  * The operands want 8 consecutive tokens of a column per lane; memory has
+//    tokens in rows.  A thread loads 8 tokens x CA (CB) columns into registers,
+//    converts the codes (v_cvt_scalef32_pk_bf16: two columns of one token
+//    share their scale), transposes pairs of tokens with v_perm and writes one
+//    16-byte operand vector per column and plane: the reads in front of the
+//    products are then 16-byte LDS reads at full rate.  Every element is
+//    converted once per workgroup.
+//  * LDS holds [plane][token group of 8][column] operand vectors; vector c of 8
+//    columns sits at c ^ (column / 8 % 8), which keeps the writes (columns CA
+//    apart) and the reads (32 adjacent columns) free of bank conflicts.
+//  * Two stages of LDS.  While stage s multiplies, stage s + 1 goes from
+//    registers to the other buffer and stage s + 2 from memory to registers;
+//    one barrier a stage, before the last 16 tokens' products, under which the
+//    first operands of the next stage are read.  The pieces of this work are
+//    placed between the products at compile time.
+//  * Tokens past T read as zero on both sides (buffer bounds; exponents by a
+//    mask, they may hold anything).  A column chunk that crosses m is read
+//    shifted, ending at m - 1, and its outputs stored accordingly.
+// ---------------------------------------------------------------------------
+typedef __bf16 wbf16x8 __attribute__((ext_vector_type(8)));
+typedef float wf32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t wu32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t wu32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWgradGroups = 256;   // workgroups that share the tiles: the compute units of an MI355X
+constexpr int kWOOB = (int)0x80000000u;
+
+template <typename TD>
+constexpr int kPlanes = 1;
+template <>
+constexpr int kPlanes<Fp16> = 2;
+template <>
+constexpr int kPlanes<float> = 3;
+
+// Tile of index idx: panels of 8 tile rows, walked down first, so that the
+// workgroups of one die (consecutive indices) share columns of both operands.
+__device__ __forceinline__ void wgrad_tile(int idx, int nbm, int nbn, int& ti, int& tj) {
+  const int panel = idx / (8 * nbn);
+  const int h = nbm - 8 * panel < 8 ? nbm - 8 * panel : 8;
+  const int r = idx - panel * 8 * nbn;
+  ti = panel * 8 + r % h;
+  tj = r / h;
+}
+
+// Work between the products, in order: A columns, A loads, B columns, B
+// loads; each with a weight of about its instructions.  slot(k) is the
+// product after which item k is placed.
+template <int CA, int CB, int P, int NB>
+struct WSched {
+  static constexpr int kItems = CA + 8 + CB + 9;
+  static constexpr int weight(int k) {
+    return k < CA ? (P == 1 ? 5 : P == 2 ? 55 : 80) : k < CA + 8 ? 2 : k < CA + 8 + CB ? 10 : 2;
+  }
+  static constexpr int before(int k) {
+    int w = 0;
+    for (int i = 0; i < k; ++i) w += weight(i);
+    return w;
+  }
+  static constexpr int slot(int k) {
+    const int total = before(kItems);
+    int span = (total + 5) / 6;   // six instructions a product
+    if (span > NB) span = NB;
+    return before(k) * span / total;
+  }
+  // first item placed at product q or later
+  static constexpr int first(int q) {
+    int k = 0;
+    while (k < kItems && slot(k) < q) ++k;
+    return k;
+  }
+};
+
+// f(integral_constant<int, B>) ... f(integral_constant<int, E - 1>)
+template <int B, int E, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    static_for<B + 1, E>(f);
+  }
+}
+
+template <typename TD, int FMT, int MT, int NT, int KT>
+struct WTile {
+  static constexpr int P = kPlanes<TD>;
+  static constexpr int SA = 64 * MT, SB = 64 * NT, KG = KT / 8, KS = KT / 16;
+  static constexpr int CA = KT * SA / 2048, CB = KT * SB / 2048;   // columns of a thread's block
+  static constexpr int NCH = 2048 / KT;                            // blocks across a tile side
+  static constexpr int kBytesA = P * KG * SA * 16, kBytesB = KG * SB * 16, kStage = kBytesA + kBytesB;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int WA = CA * (int)sizeof(TD) / 4;              // words of a row of a block
+  static constexpr int WB = CB / 4;
+  static constexpr int PS = P * MT * NT;                           // products of 16 tokens
+  static constexpr int NB = (KS - 1) * PS;                         // products in front of the barrier
+};
+
+// n words from a buffer at a byte offset (zero past its end).
+template <int N>
+__device__ __forceinline__ void buffer_words(__amdgpu_buffer_rsrc_t rs, int off, uint32_t* w) {
+  if constexpr (N == 4) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = v[i];
+  } else if constexpr (N == 2) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
+    w[0] = v[0];
+    w[1] = v[1];
+  } else {
+    w[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
+  }
+}
+
+// What x leaves after its leading 8 bits (zero for an infinity; NaN stays NaN).
+__device__ __forceinline__ float bf16_rest(float x) {
+  const float r = x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+  return __builtin_fabsf(x) == __builtin_inff() ? 0.f : r;
+}
+
+// Element c (0 or 1) of a word of two fp16.
+__device__ __forceinline__ float half_of(uint32_t w, int c) {
+  const f16x2 h = __builtin_bit_cast(f16x2, w);
+  return (float)h[c];
+}
+
+// Output row of tile row i (both from the tile's first row), -1 if it is not
+// this row's to write: the chunk of ca rows that crosses the last row mi - 1
+// was read shifted up to end there.
+__device__ __forceinline__ int wgrad_row(int i, int ca, int mi) {
+  const int cb = i & ~(ca - 1);
+  if (cb + ca > mi) i += mi - ca - cb;
+  return i >= cb && i < mi ? i : -1;
+}
+
+template <typename TD, int FMT, int MT, int NT, int KT>
+__device__ __forceinline__ void wgrad_segment(const WgradArgs& a, char* lds, int ti, int tj, int s_a, int s_b,
+                                              float* part) {
+  using C = WTile<TD, FMT, MT, NT, KT>;
+  constexpr int P = C::P;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int i0 = ti * C::SA, j0 = tj * C::SB;
+  // this thread's block: 8 tokens of group kg, columns ch CA .. and ch CB ..
+  const int ch = tid % C::NCH, kg = tid / C::NCH;
+  int offa[8], offb[8], offs;
+  {
+    int ca = i0 + ch * C::CA;
+    if (ca > a.m - C::CA) ca = a.m - C::CA;
+    const int cb = j0 + ch * C::CB;
+    const bool in = cb < a.nb * kActBlock;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      offa[r] = (int)(((kg * 8 + r) * a.ldd + ca) * (int64_t)sizeof(TD));
+      offb[r] = in ? (int)((kg * 8 + r) * a.ldc + cb) : kWOOB;
+    }
+    offs = in ? (kg * a.nb + cb / kActBlock) * kActGroup : kWOOB;
+  }
+  // LDS byte addresses of column 0 of the block; column c is at ^ (16 c)
+  auto vec_addr = [](int kgrp, int col, int side) {
+    return (kgrp * side + (col & ~7) + ((col ^ (col >> 3)) & 7)) * 16;
+  };
+  const int wra = vec_addr(kg, ch * C::CA, C::SA), wrb = vec_addr(kg, ch * C::CB, C::SB) + C::kBytesA;
+  // operand reads: [tile parity]
+  int rda[2], rdb[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    rda[q] = vec_addr(lane >> 5, wm * 32 * MT + 32 * q + (lane & 31), C::SA);
+    rdb[q] = vec_addr(lane >> 5, wn * 32 * NT + 32 * q + (lane & 31), C::SB) + C::kBytesA;
+  }
+
+  uint32_t ra[8][C::WA], rb[8][C::WB], re[2];
+  uint32_t bv[8];   // a pair of converted columns, 8 tokens
+  struct Rsrc {
+    __amdgpu_buffer_rsrc_t a, b, s;
+    int rows;   // tokens of the stage
+  };
+  const uint32_t lda = (uint32_t)(a.ldd * (int64_t)sizeof(TD)), ldb = (uint32_t)a.ldc;   // bytes
+  const uint32_t wa = (uint32_t)a.m * (uint32_t)sizeof(TD), wb = (uint32_t)a.nb * kActBlock;
+  const int tail = (int)(a.T - (int64_t)(a.nst - 1) * KT);
+  // buffers of the next stage to load; past s_b: no bytes, the loads give zeros
+  int st_next = s_a;
+  const char* pa = static_cast<const char*>(a.delta) + (int64_t)s_a * KT * lda;
+  const uint8_t* pb = a.codes + (int64_t)s_a * KT * ldb;
+  const uint8_t* ps = a.bscales + (int64_t)s_a * KT * a.nb;
+  auto next_stage = [&]() {
+    Rsrc R;
+    const bool in = st_next < s_b, full = st_next < a.nst - 1;
+    R.rows = full ? KT : tail;
+    const uint32_t last = (uint32_t)R.rows - 1;
+    R.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(pa), (short)0, in ? (int)(last * lda + wa) : 0, 0x00020000);
+    R.b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pb), (short)0, in ? (int)(last * ldb + wb) : 0,
+                                            0x00020000);
+    R.s = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ps), (short)0,
+                                            in ? (int)((last / 8 + 1) * (uint32_t)a.nb * kActGroup) : 0, 0x00020000);
+    if (st_next < s_b) {
+      ++st_next;
+      pa += (uint64_t)KT * lda;
+      pb += (uint64_t)KT * ldb;
+      ps += (uint64_t)KT * (uint32_t)a.nb;
+    }
+    return R;
+  };
+  int nleft = 0;   // valid tokens of the stage held in registers
+  auto load_a = [&](const Rsrc& R, int r) { buffer_words<C::WA>(R.a, offa[r], ra[r]); };
+  auto load_b = [&](const Rsrc& R, int r) {
+    if (r < 8) {
+      buffer_words<C::WB>(R.b, offb[r], rb[r]);
+    } else {
+      buffer_words<2>(R.s, offs, re);
+      nleft = R.rows;
+    }
+  };
+  auto put = [&](int addr, const uint32_t* w) {
+    const wu32x4 v = {w[0], w[1], w[2], w[3]};
+    *reinterpret_cast<wu32x4*>(lds + addr) = v;
+  };
+  auto conv_a = [&](int c, int base) {
+    const int at = base + (wra ^ (c << 4));
+    if constexpr (P == 1) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = __builtin_amdgcn_perm(ra[2 * k + 1][c / 2], ra[2 * k][c / 2], c & 1 ? 0x07060302u : 0x05040100u);
+      put(at, w);
+    } else {
+      uint32_t w[P][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x, y;
+        if constexpr (P == 2) {
+          x = half_of(ra[2 * k][c / 2], c & 1);
+          y = half_of(ra[2 * k + 1][c / 2], c & 1);
+        } else {
+          x = __uint_as_float(ra[2 * k][c]);
+          y = __uint_as_float(ra[2 * k + 1][c]);
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          w[p][k] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+          if (p + 1 < P) {
+            x = bf16_rest(x);
+            y = bf16_rest(y);
+          }
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) put(at + p * C::KG * C::SA * 16, w[p]);
+    }
+  };
+  auto conv_b = [&](int c, int base) {
+    if ((c & 1) == 0) {
+      if (c == 0) {
+        // exponents of tokens past T may hold anything: zero
+        const int n = nleft - kg * 8;
+        re[0] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+        re[1] &= n >= 8 ? ~0u : n <= 4 ? 0u : (1u << (8 * (n - 4))) - 1u;
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float s = act_scale((re[r / 4] >> (8 * (r % 4))) & 0xFFu);
+        const bool hi = (c & 2) != 0;
+        bf16x2 v;
+        if constexpr (FMT == 0) v = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(rb[r][c / 4], s, true)
+                                       : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(rb[r][c / 4], s, false);
+        else v = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(rb[r][c / 4], s, true)
+                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(rb[r][c / 4], s, false);
+        bv[r] = __builtin_bit_cast(uint32_t, v);
+      }
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = __builtin_amdgcn_perm(bv[2 * k + 1], bv[2 * k], c & 1 ? 0x07060302u : 0x05040100u);
+    put(base + (wrb ^ (c << 4)), w);
+  };
+
+  wf32x16 acc[MT][NT];
+#pragma unroll
+  for (int x = 0; x < MT; ++x)
+#pragma unroll
+    for (int y = 0; y < NT; ++y)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.f;
+  struct Frags {
+    wbf16x8 a[P][MT], b[NT];
+  };
+  // operand read k of 16 tokens: B tiles first, then A tiles of each plane
+  auto read_frag = [&](Frags& F, int base, int ks, int k) {
+    if (k < NT) {
+      F.b[k] = *reinterpret_cast<const wbf16x8*>(lds + base + rdb[k & 1] + (k >> 1) * 1024 + ks * 2 * C::SB * 16);
+    } else if (k < NT + P * MT) {
+      const int p = (k - NT) / MT, t = (k - NT) % MT;
+      F.a[p][t] = *reinterpret_cast<const wbf16x8*>(lds + base + rda[t & 1] + (t >> 1) * 1024 +
+                                                    (p * C::KG + ks * 2) * C::SA * 16);
+    }
+  };
+  using S = WSched<C::CA, C::CB, P, C::NB>;
+
+  __syncthreads();   // the previous segment's waves are done with the LDS
+  {
+    const Rsrc R = next_stage(), R1 = next_stage();
+#pragma unroll
+    for (int r = 0; r < 8; ++r) load_a(R, r);
+#pragma unroll
+    for (int r = 0; r < 9; ++r) load_b(R, r);
+#pragma unroll
+    for (int c = 0; c < C::CA; ++c) conv_a(c, 0);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) load_a(R1, r);
+#pragma unroll
+    for (int c = 0; c < C::CB; ++c) conv_b(c, 0);
+#pragma unroll
+    for (int r = 0; r < 9; ++r) load_b(R1, r);
+  }
+  __syncthreads();
+  Frags F[2];
+#pragma unroll
+  for (int k = 0; k < NT + P * MT; ++k) read_frag(F[0], 0, 0, k);
+  int base = 0;
+  for (int st = s_a; st < s_b; ++st) {
+    const int nbase = base ^ C::kStage;
+    const Rsrc R = next_stage();
+static_for<0, C::KS>([&](auto KSC) {
+      constexpr int ks = decltype(KSC)::value;
+      constexpr bool last = ks == C::KS - 1;
+      if constexpr (last) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this wave's part of the next stage is written
+        __syncthreads();
+      }
+      static_for<0, C::PS>([&](auto QC) {
+        constexpr int q = decltype(QC)::value, p = q / (MT * NT), x = q / NT % MT, y = q % NT, n = ks * C::PS + q;
+        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(F[ks & 1].a[p][x], F[ks & 1].b[y], acc[x][y], 0, 0, 0);
+        read_frag(F[(ks + 1) & 1], last ? nbase : base, last ? 0 : ks + 1, q);
+        static_for<S::first(n), S::first(n + 1)>([&](auto KC) {
+          constexpr int k = decltype(KC)::value;
+          if constexpr (k < C::CA) conv_a(k, nbase);
+          else if constexpr (k < C::CA + 8) load_a(R, k - C::CA);
+          else if constexpr (k < C::CA + 8 + C::CB) conv_b(k - C::CA - 8, nbase);
+          else load_b(R, k - C::CA - 8 - C::CB);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    base = nbase;
+  }
+
+  // Register e of MFMA tile (x, y) is element (8 (e / 4) + 4 (lane / 32) + e %
+  // 4, lane % 32) of the 32 x 32 outputs.  One path for W and for a segment
+  // (a whole [SA][SB] tile): two would keep copies of all sums.
+  float* out = part ? part : a.W + (int64_t)i0 * a.ldw + j0;
+  const int64_t ldo = part ? C::SB : a.ldw;
+  const int mi = part ? C::SA : a.m - i0, nj = part ? C::SB : a.d - j0;
+  const float alpha = part ? 1.f : a.alpha;
+  const bool add = !part && a.accumulate;
+  // the sums stay in the accumulator registers until their own turn
+  auto hold = [](wf32x16& v) {
+    if constexpr (MT * NT > 4) asm volatile("" : "+a"(v));
+  };
+#pragma unroll
+  for (int x = 0; x < MT; ++x)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int i = wgrad_row(32 * (wm * MT + x) + 8 * (e / 4) + 4 * (lane >> 5) + e % 4, C::CA, mi);
+      float* row = out + (int64_t)i * ldo;
+#pragma unroll
+      for (int y = 0; y < NT; ++y) {
+        const int j = 32 * (wn * NT + y) + (lane & 31);
+        hold(acc[x][y]);
+        float v = alpha * acc[x][y][e];
+        if (i >= 0 && j < nj) {
+          if (add) v += row[j];
+          row[j] = v;
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// Workgroup g (consecutive numbers on one die) first takes whole tiles in
+// rounds; the tiles left over, fewer than there are workgroups, are cut into
+// equal contiguous ranges of (tile, stage).  A range that is not a whole tile
+// goes to part, segment number g + tile, and k_wgrad_join adds the segments
+// of a tile in order: no atomics, the same sums every time.
+template <typename TD, int FMT, int MT, int NT, int KT>
+__global__ void __launch_bounds__(256, MT * NT > 4 ? 1 : 2) k_wgrad(WgradArgs a) {
+  using C = WTile<TD, FMT, MT, NT, KT>;
+  __shared__ __attribute__((aligned(16))) char lds[C::kLds];
+  const int G = gridDim.x;
+  const int g = G % 8 == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+  const int whole = a.rounds * G, tiles = a.nbm * a.nbn;
+  const int64_t U = (int64_t)(tiles - whole) * a.nst;
+  const int64_t u0 = U * g / G, u1 = U * (g + 1) / G;
+  // the range: its first tile and stage, its stages (divisions run on the
+  // vector units: the compiler is told that the results are uniform)
+  int left = __builtin_amdgcn_readfirstlane((int)(u0 / a.nst));
+  int s_a = __builtin_amdgcn_readfirstlane((int)(u0 % a.nst));
+  int n = __builtin_amdgcn_readfirstlane((int)(u1 - u0));
+  for (int rd = 0; rd < a.rounds || n > 0; ++rd) {
+    const bool full = rd < a.rounds;
+    const int tile = full ? rd * G + g : whole + left;
+    const int s0 = full ? 0 : s_a, s1 = full || n >= a.nst - s_a ? a.nst : s_a + n;
+    const bool split = s0 > 0 || s1 < a.nst;
+    int ti, tj;
+    wgrad_tile(tile, a.nbm, a.nbn, ti, tj);
+    wgrad_segment<TD, FMT, MT, NT, KT>(a, lds, __builtin_amdgcn_readfirstlane(ti), __builtin_amdgcn_readfirstlane(tj),
+                                       s0, s1, split ? a.part + (int64_t)(g + left) * C::SA * C::SB : nullptr);
+    if (!full) {
+      n -= s1 - s0;
+      s_a = 0;
+      ++left;
+    }
+  }
+}
+
+// W of the split tiles from their segments, added in token order.  Each
+// workgroup takes 1024 elements of one tile, four a thread.
+template <int MT, int NT>
+__global__ void __launch_bounds__(256) k_wgrad_join(WgradArgs a, int G, int ca) {
+  constexpr int SA = 64 * MT, SB = 64 * NT, PER = MT * NT * 4;   // workgroups of a tile
+  const int left = blockIdx.x / PER, q = blockIdx.x % PER;
+  const int whole = a.rounds * G, tiles = a.nbm * a.nbn;
+  const int64_t U = (int64_t)(tiles - whole) * a.nst;
+  // workgroups whose ranges meet [left nst, (left + 1) nst): first holds its start, last its end
+  const int64_t b = (int64_t)left * a.nst, e = b + a.nst;
+  int first = (int)(b * G / U), last = (int)((e - 1) * G / U);
+  while (U * (first + 1) / G <= b) ++first;
+  while (U * (last + 1) / G < e) ++last;
+  if (first == last) return;   // written by its workgroup
+  const int f = (q * 256 + threadIdx.x) * 4;
+  const float* p = a.part + (int64_t)(first + left) * SA * SB + f;
+  float4 s = *reinterpret_cast<const float4*>(p);
+  for (int k = first + 1; k <= last; ++k) {
+    p += SA * SB;
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  int ti, tj;
+  wgrad_tile(whole + left, a.nbm, a.nbn, ti, tj);
+  const int i = wgrad_row(f / SB, ca, a.m - ti * SA), j = tj * SB + f % SB;
+  if (i < 0) return;
+  float* w = a.W + (int64_t)(ti * SA + i) * a.ldw + j;
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (j + r < a.d) {
+      const float o = a.alpha * v[r];
+      w[r] = a.accumulate ? w[r] + o : o;
+    }
+}
 
 // 64 x 64 outputs per workgroup, 32 tokens per LDS stage, 4 x 4 outputs per
 // thread, fp32 products and sums over 256 tokens, folded into fp64.
@@ -95,6 +561,61 @@ __global__ void __launch_bounds__(256) k_wgrad_valu(WgradArgs a) {
   }
 }
 
+
+namespace {
+
+struct WgradPlan {
+  int variant;         // 0: vector units, 1: 256 x 256 tiles, 2: 128 x 128
+  int kt, side, nbm, nbn, nst, rounds, grid;
+  int64_t split;       // tiles cut into segments
+  size_t bytes;
+};
+
+WgradPlan wgrad_plan(int64_t T, int m, int d, int dtype, int64_t ldd, int64_t ldc) {
+  WgradPlan p{};
+  const int size = dtype == GIFT_FP32 ? 4 : 2;
+  if (m < 8 || 64 * ldd * size >= ((int64_t)1 << 31) || 64 * ldc >= ((int64_t)1 << 31) || T == 0) return p;
+  p.variant = cdiv(m, 256) * cdiv(d, 256) >= 32 ? 1 : 2;
+  p.side = p.variant == 1 ? 256 : 128;
+  p.kt = p.variant == 1 && dtype != GIFT_BF16 ? 32 : 64;
+  p.nbm = (int)cdiv(m, p.side);
+  p.nbn = (int)cdiv(d, p.side);
+  p.nst = (int)cdiv(T, p.kt);
+  const int64_t tiles = (int64_t)p.nbm * p.nbn;
+  const int G = kWgradGroups;
+  const int64_t units = tiles * p.nst;
+  p.grid = (int)(units < G ? units : G);
+  p.rounds = (int)(tiles / p.grid);
+  p.split = tiles - (int64_t)p.rounds * p.grid;
+  p.bytes = p.split ? (size_t)(p.split + p.grid) * p.side * p.side * 4 : 0;
+  return p;
+}
+
+template <typename TD, int FMT, int MT, int KT>
+void wgrad_go(const WgradArgs& a, const WgradPlan& p, hipStream_t s) {
+  hipLaunchKernelGGL((k_wgrad<TD, FMT, MT, MT, KT>), dim3((unsigned)p.grid), dim3(256), 0, s, a);
+  if (p.split)
+    hipLaunchKernelGGL((k_wgrad_join<MT, MT>), dim3((unsigned)(p.split * MT * MT * 4)), dim3(256), 0, s, a, p.grid,
+                       KT * MT / 32);
+}
+
+template <typename TD, int KT>
+void wgrad_t(const WgradArgs& a, const WgradPlan& p, hipStream_t s) {
+  if (p.variant == 1) {
+    if (a.fmt == GIFT_E4M3) wgrad_go<TD, 0, 4, KT>(a, p, s);
+    else wgrad_go<TD, 1, 4, KT>(a, p, s);
+  } else {
+    if (a.fmt == GIFT_E4M3) wgrad_go<TD, 0, 2, 64>(a, p, s);
+    else wgrad_go<TD, 1, 2, 64>(a, p, s);
+  }
+}
+
+}  // namespace
+
+size_t wgrad_workspace(int64_t T, int m, int d, int dtype) {
+  return align256(wgrad_plan(T, m, d, dtype, 0, 0).bytes) + 256;
+}
+
 hipError_t launch_weight_grad(const WgradCall& c, hipStream_t s) {
   WgradArgs a{};
   a.delta = c.delta;
@@ -112,10 +633,22 @@ hipError_t launch_weight_grad(const WgradCall& c, hipStream_t s) {
   a.W = c.W;
   a.ldw = c.ldw;
   if (c.T == 0 && c.accumulate) return hipSuccess;
-  const dim3 grid((unsigned)(cdiv(c.m, 64) * cdiv(c.d, 64)));
-  if (c.dtype == GIFT_BF16) hipLaunchKernelGGL(k_wgrad_valu<Bf16>, grid, dim3(256), 0, s, a);
-  else if (c.dtype == GIFT_FP16) hipLaunchKernelGGL(k_wgrad_valu<Fp16>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_wgrad_valu<float>, grid, dim3(256), 0, s, a);
+  const WgradPlan p = wgrad_plan(c.T, c.m, c.d, c.dtype, c.ldd, c.ckpt->ldc);
+  if (p.variant == 0) {
+    const dim3 grid((unsigned)(cdiv(c.m, 64) * cdiv(c.d, 64)));
+    if (c.dtype == GIFT_BF16) hipLaunchKernelGGL(k_wgrad_valu<Bf16>, grid, dim3(256), 0, s, a);
+    else if (c.dtype == GIFT_FP16) hipLaunchKernelGGL(k_wgrad_valu<Fp16>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(k_wgrad_valu<float>, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  a.part = c.work;
+  a.nst = p.nst;
+  a.nbm = p.nbm;
+  a.nbn = p.nbn;
+  a.rounds = p.rounds;
+  if (c.dtype == GIFT_BF16) wgrad_t<Bf16, 64>(a, p, s);
+  else if (c.dtype == GIFT_FP16) wgrad_t<Fp16, 32>(a, p, s);
+  else wgrad_t<float, 32>(a, p, s);
   return hipGetLastError();
 }
 
