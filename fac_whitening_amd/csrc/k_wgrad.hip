@@ -27,8 +27,57 @@ struct WgradArgs {
   float* part;             // segments of tiles split over workgroups
   int nst;                 // token stages of a tile
   int nbm, nbn;            // output tiles down and across
-  int rounds;              // whole tiles of each workgroup
+  int unit;                // stages of a unit: tiles are split at whole units
 };
+
+// How G workgroups share R tiles of n units each: in levels, each a set of
+// pieces of one length that start at one place of the token axis, so that
+// workgroups on one die walk the same tokens at the same time and share them
+// through its L2.  With C = ceil(R n / G) units for every workgroup:
+//   n >= C: q = n / C workgroups a tile take C units each and are done
+//   n <  C: every workgroup takes all n units of C / n tiles
+// and what is left of tiles, units, workgroups and C goes through the same
+// step again (the Euclidean algorithm on n and C).  Pieces of a level are
+// numbered from `base`; piece 0 .. R - 1 of a level is that of its tile.
+struct WLevel {
+  int R, n, W, C;      // tiles, units left of each, workgroups, units left for each
+  int from;            // first unit of the pieces
+  int tile0;           // first tile
+  int base;            // number of the level's first piece
+  __host__ __device__ bool done() const { return R == 0 || n == 0; }
+  __host__ __device__ bool split() const { return n >= C; }            // pieces of C units, count() a tile
+  __host__ __device__ int count() const { return split() ? n / C : C / n; }
+  __host__ __device__ int tiles() const {                              // tiles that are finished at this level
+    const int64_t t = split() ? R : (int64_t)count() * W;
+    return t < R ? (int)t : R;
+  }
+  __host__ __device__ void next() {
+    if (split()) {
+      const int q = n / C;
+      base += q * R;
+      W -= q * R;
+      from += q * C;
+      n -= q * C;
+    } else {
+      const int t = tiles();
+      base += t;
+      C -= count() * n;
+      R -= t;
+      tile0 += t;
+    }
+  }
+};
+
+// The first level.  Pieces of whole tiles are written to W directly and have
+// no number.
+__host__ __device__ inline WLevel wgrad_levels(int tiles, int units, int G) {
+  WLevel v{};
+  v.R = tiles;
+  v.n = units;
+  v.W = G;
+  v.C = (int)(((int64_t)tiles * units + G - 1) / G);
+  return v;
+}
 
 __device__ __forceinline__ float elem_f32(const float* p) { return *p; }
 __device__ __forceinline__ float elem_f32(const Bf16* p) { return __uint_as_float((uint32_t)p->v << 16); }
@@ -86,31 +135,57 @@ __device__ __forceinline__ void wgrad_tile(int idx, int nbm, int nbn, int& ti, i
   tj = r / h;
 }
 
-// Work between the products, in order: A columns, A loads, B columns, B
-// loads; each with a weight of about its instructions.  slot(k) is the
-// product after which item k is placed.
-template <int CA, int CB, int P, int NB>
+// Work between the products.  A wave issues in order and is alone on its
+// SIMD: a product starts late when what is issued in front of it takes longer
+// than the product before (32 clocks).  So the work is cut into small items
+// and a slot, what follows one product, takes items up to `cap` clocks, the
+// least that places all conversions in front of the barrier.  Measured: a
+// 16-byte LDS write holds the issue for 20 clocks, other instructions 4.
+//   items 0 .. kA - 1: column c of A, kParts steps and P writes
+//   .. kCols - 1: scales of 4 + 4 tokens, then for each pair of B columns
+//   four steps of two tokens and two writes
+//   .. kItems - 1: 8 A and 9 B loads, one every few of all N products (in a
+//   burst they fill the memory pipe's queue and stop the wave), each after
+//   the steps that empty its registers
+// After product n come the items order[begin[n]] .. order[begin[n + 1] - 1].
+template <int CA, int CB, int P, int NB, int N, int KS, int READS>
 struct WSched {
-  static constexpr int kItems = CA + 8 + CB + 9;
-  static constexpr int weight(int k) {
-    return k < CA ? (P == 1 ? 5 : P == 2 ? 55 : 80) : k < CA + 8 ? 2 : k < CA + 8 + CB ? 10 : 2;
+  static constexpr int kParts = P == 1 ? 1 : 4, kPerA = kParts + P;
+  static constexpr int kA = CA * kPerA, kCols = kA + 2 + CB * 3, kItems = kCols + 17;
+  int slot[kItems] = {}, begin[N + 1] = {}, order[kItems] = {}, cap = 0;
+  static constexpr int cost(int k) {
+    if (k < kA) return k % kPerA >= kParts ? 20 : P == 1 ? 16 : P == 2 ? 48 : 76;
+    if (k < kA + 2) return 32;
+    return (k - kA - 2) % 6 >= 4 ? 20 : 16;
   }
-  static constexpr int before(int k) {
-    int w = 0;
-    for (int i = 0; i < k; ++i) w += weight(i);
-    return w;
+  constexpr bool place(int c) {
+    int k = 0, load = 0, a_end = N, b_end = N;
+    for (int n = 0; n < N; ++n) {
+      int used = n % (N / KS) < READS ? 4 : 0;
+      if (load < 17 && n > (load < 8 ? a_end : b_end) && n >= a_end + 1 + load * (N - a_end - 1) / 17) {
+        slot[kCols + load++] = n;
+        used += 8;
+      }
+      for (int first = 1; k < kCols && (first || used + cost(k) <= c); first = 0) {
+        if (used + cost(k) > c && cost(k) <= c) break;
+        used += cost(k);
+        if (k == kA - 1) a_end = n;
+        if (k == kCols - 1) b_end = n;
+        slot[k++] = n;
+      }
+    }
+    while (load < 17) slot[kCols + load++] = N - 1;
+    return k == kCols && slot[kCols - 1] < NB - 2;   // (the last writes have time to end)
   }
-  static constexpr int slot(int k) {
-    const int total = before(kItems);
-    int span = (total + 5) / 6;   // six instructions a product
-    if (span > NB) span = NB;
-    return before(k) * span / total;
-  }
-  // first item placed at product q or later
-  static constexpr int first(int q) {
-    int k = 0;
-    while (k < kItems && slot(k) < q) ++k;
-    return k;
+  constexpr WSched() {
+    for (cap = 20; !place(cap); cap += 2) {}
+    int at = 0;
+    for (int n = 0; n < N; ++n) {
+      begin[n] = at;
+      for (int k = 0; k < kItems; ++k)
+        if (slot[k] == n) order[at++] = k;
+    }
+    begin[N] = at;
   }
 };
 
@@ -179,23 +254,25 @@ __device__ __forceinline__ void wgrad_segment(const WgradArgs& a, char* lds, int
                                               float* part) {
   using C = WTile<TD, FMT, MT, NT, KT>;
   constexpr int P = C::P;
-  const int tid = threadIdx.x, lane = tid & 63;
+  // (opaque, here and for the epilogue: what depends on the lane is computed
+  // again for each piece instead of being kept in registers over all of them)
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int i0 = ti * C::SA, j0 = tj * C::SB;
   // this thread's block: 8 tokens of group kg, columns ch CA .. and ch CB ..
   const int ch = tid % C::NCH, kg = tid / C::NCH;
-  int offa[8], offb[8], offs;
+  const uint32_t lda = (uint32_t)(a.ldd * (int64_t)sizeof(TD)), ldb = (uint32_t)a.ldc;   // bytes
+  int offa, offb, offs;   // of the block's first row
   {
     int ca = i0 + ch * C::CA;
     if (ca > a.m - C::CA) ca = a.m - C::CA;
     const int cb = j0 + ch * C::CB;
     const bool in = cb < a.nb * kActBlock;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      offa[r] = (int)(((kg * 8 + r) * a.ldd + ca) * (int64_t)sizeof(TD));
-      offb[r] = in ? (int)((kg * 8 + r) * a.ldc + cb) : kWOOB;
-    }
+    offa = (int)((uint32_t)(kg * 8) * lda) + ca * (int)sizeof(TD);
+    offb = in ? (int)((uint32_t)(kg * 8) * ldb) + cb : kWOOB;   // (stays past the end with any row added)
     offs = in ? (kg * a.nb + cb / kActBlock) * kActGroup : kWOOB;
   }
   // LDS byte addresses of column 0 of the block; column c is at ^ (16 c)
@@ -211,15 +288,25 @@ __device__ __forceinline__ void wgrad_segment(const WgradArgs& a, char* lds, int
     rdb[q] = vec_addr(lane >> 5, wn * 32 * NT + 32 * q + (lane & 31), C::SB) + C::kBytesA;
   }
 
-  uint32_t ra[8][C::WA], rb[8][C::WB], re[2];
-  uint32_t bv[8];   // a pair of converted columns, 8 tokens
+  struct Raw {
+    uint32_t a[8][C::WA], b[8][C::WB], e[2];
+    int rows;   // tokens of the stage
+  };
+  // two stages of loads in flight (one where three planes of a 256 x 256 tile leave no registers for it)
+  constexpr int SETS = P == 3 && MT * NT > 4 ? 1 : 2;
+  Raw raw[SETS];
+  uint32_t bv[2][4];   // a pair of converted columns, 8 tokens
+  float sc[8];         // scales of the tokens
   struct Rsrc {
     __amdgpu_buffer_rsrc_t a, b, s;
     int rows;   // tokens of the stage
   };
-  const uint32_t lda = (uint32_t)(a.ldd * (int64_t)sizeof(TD)), ldb = (uint32_t)a.ldc;   // bytes
   const uint32_t wa = (uint32_t)a.m * (uint32_t)sizeof(TD), wb = (uint32_t)a.nb * kActBlock;
+  // bytes of a whole stage and of the last one, which may hold fewer tokens
   const int tail = (int)(a.T - (int64_t)(a.nst - 1) * KT);
+  const uint32_t za = (uint32_t)(KT - 1) * lda + wa, zat = (uint32_t)(tail - 1) * lda + wa;
+  const uint32_t zb = (uint32_t)(KT - 1) * ldb + wb, zbt = (uint32_t)(tail - 1) * ldb + wb;
+  const uint32_t zs = (uint32_t)C::KG * a.nb * kActGroup, zst = (uint32_t)((tail + 7) / 8) * a.nb * kActGroup;
   // buffers of the next stage to load; past s_b: no bytes, the loads give zeros
   int st_next = s_a;
   const char* pa = static_cast<const char*>(a.delta) + (int64_t)s_a * KT * lda;
@@ -229,93 +316,92 @@ __device__ __forceinline__ void wgrad_segment(const WgradArgs& a, char* lds, int
     Rsrc R;
     const bool in = st_next < s_b, full = st_next < a.nst - 1;
     R.rows = full ? KT : tail;
-    const uint32_t last = (uint32_t)R.rows - 1;
-    R.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(pa), (short)0, in ? (int)(last * lda + wa) : 0, 0x00020000);
-    R.b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pb), (short)0, in ? (int)(last * ldb + wb) : 0,
+    R.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(pa), (short)0, in ? (int)(full ? za : zat) : 0, 0x00020000);
+    R.b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pb), (short)0, in ? (int)(full ? zb : zbt) : 0,
                                             0x00020000);
-    R.s = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ps), (short)0,
-                                            in ? (int)((last / 8 + 1) * (uint32_t)a.nb * kActGroup) : 0, 0x00020000);
-    if (st_next < s_b) {
-      ++st_next;
-      pa += (uint64_t)KT * lda;
-      pb += (uint64_t)KT * ldb;
-      ps += (uint64_t)KT * (uint32_t)a.nb;
-    }
+    R.s = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ps), (short)0, in ? (int)(full ? zs : zst) : 0,
+                                            0x00020000);
+    ++st_next;
+    pa += (uint64_t)KT * lda;
+    pb += (uint64_t)KT * ldb;
+    ps += (uint64_t)KT * (uint32_t)a.nb;
     return R;
   };
-  int nleft = 0;   // valid tokens of the stage held in registers
-  auto load_a = [&](const Rsrc& R, int r) { buffer_words<C::WA>(R.a, offa[r], ra[r]); };
-  auto load_b = [&](const Rsrc& R, int r) {
+  // (one addition at each load, opaque: kept as values they would take sixteen registers)
+  auto row_off = [](int off, uint32_t r) {
+    int o;
+    asm volatile("v_add_u32 %0, %1, %2" : "=v"(o) : "s"(r), "v"(off));
+    return o;
+  };
+  auto load_a = [&](Raw& x, const Rsrc& R, int r) { buffer_words<C::WA>(R.a, row_off(offa, r * lda), x.a[r]); };
+  auto load_b = [&](Raw& x, const Rsrc& R, int r) {
     if (r < 8) {
-      buffer_words<C::WB>(R.b, offb[r], rb[r]);
+      buffer_words<C::WB>(R.b, row_off(offb, r * ldb), x.b[r]);
     } else {
-      buffer_words<2>(R.s, offs, re);
-      nleft = R.rows;
+      buffer_words<2>(R.s, offs, x.e);
+      x.rows = R.rows;
     }
   };
   auto put = [&](int addr, const uint32_t* w) {
     const wu32x4 v = {w[0], w[1], w[2], w[3]};
     *reinterpret_cast<wu32x4*>(lds + addr) = v;
   };
-  auto conv_a = [&](int c, int base) {
-    const int at = base + (wra ^ (c << 4));
-    if constexpr (P == 1) {
-      uint32_t w[4];
+  // column c of A: token pairs `part` (-1: all) to the planes; then the write of each plane
+  uint32_t wv[P][4];
+  auto conv_a = [&](Raw& raw, int c, int part) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = __builtin_amdgcn_perm(ra[2 * k + 1][c / 2], ra[2 * k][c / 2], c & 1 ? 0x07060302u : 0x05040100u);
-      put(at, w);
-    } else {
-      uint32_t w[P][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4; ++k) {
+      if (part >= 0 && k != part) continue;
+      if constexpr (P == 1) {
+        wv[0][k] = __builtin_amdgcn_perm(raw.a[2 * k + 1][c / 2], raw.a[2 * k][c / 2], c & 1 ? 0x07060302u : 0x05040100u);
+      } else {
         float x, y;
         if constexpr (P == 2) {
-          x = half_of(ra[2 * k][c / 2], c & 1);
-          y = half_of(ra[2 * k + 1][c / 2], c & 1);
+          x = half_of(raw.a[2 * k][c / 2], c & 1);
+          y = half_of(raw.a[2 * k + 1][c / 2], c & 1);
         } else {
-          x = __uint_as_float(ra[2 * k][c]);
-          y = __uint_as_float(ra[2 * k + 1][c]);
+          x = __uint_as_float(raw.a[2 * k][c]);
+          y = __uint_as_float(raw.a[2 * k + 1][c]);
         }
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          w[p][k] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+          wv[p][k] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
           if (p + 1 < P) {
             x = bf16_rest(x);
             y = bf16_rest(y);
           }
         }
       }
-#pragma unroll
-      for (int p = 0; p < P; ++p) put(at + p * C::KG * C::SA * 16, w[p]);
     }
   };
-  auto conv_b = [&](int c, int base) {
-    if ((c & 1) == 0) {
-      if (c == 0) {
-        // exponents of tokens past T may hold anything: zero
-        const int n = nleft - kg * 8;
-        re[0] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-        re[1] &= n >= 8 ? ~0u : n <= 4 ? 0u : (1u << (8 * (n - 4))) - 1u;
-      }
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const float s = act_scale((re[r / 4] >> (8 * (r % 4))) & 0xFFu);
-        const bool hi = (c & 2) != 0;
-        bf16x2 v;
-        if constexpr (FMT == 0) v = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(rb[r][c / 4], s, true)
-                                       : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(rb[r][c / 4], s, false);
-        else v = hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(rb[r][c / 4], s, true)
-                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(rb[r][c / 4], s, false);
-        bv[r] = __builtin_bit_cast(uint32_t, v);
-      }
+  auto put_a = [&](int c, int p, int base) { put(base + (wra ^ (c << 4)) + p * C::KG * C::SA * 16, wv[p]); };
+  // scales of tokens 4 h .. 4 h + 3; exponents of tokens past T may hold anything: zero
+  auto scale_b = [&](Raw& raw, int h) {
+    uint32_t e = raw.e[h];
+    if (raw.rows < KT) {
+      const int n = raw.rows - kg * 8 - 4 * h;
+      e &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
     }
-    uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = __builtin_amdgcn_perm(bv[2 * k + 1], bv[2 * k], c & 1 ? 0x07060302u : 0x05040100u);
-    put(base + (wrb ^ (c << 4)), w);
+    for (int r = 0; r < 4; ++r) sc[4 * h + r] = act_scale((e >> (8 * r)) & 0xFFu);
   };
+  // columns 2 c, 2 c + 1 of B: token pairs `part`; then the write of each
+  auto conv_b = [&](Raw& raw, int c, int part) {
+    uint32_t v[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int r = 2 * part + t;
+      bf16x2 x;
+      if constexpr (FMT == 0) x = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.b[r][c / 2], sc[r], true)
+                                        : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw.b[r][c / 2], sc[r], false);
+      else x = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(raw.b[r][c / 2], sc[r], true)
+                     : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(raw.b[r][c / 2], sc[r], false);
+      v[t] = __builtin_bit_cast(uint32_t, x);
+    }
+    bv[0][part] = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);
+    bv[1][part] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
+  };
+  auto put_b = [&](int c, int h, int base) { put(base + (wrb ^ (c << 5) ^ (h << 4)), bv[h]); };
 
   wf32x16 acc[MT][NT];
 #pragma unroll
@@ -337,33 +423,48 @@ __device__ __forceinline__ void wgrad_segment(const WgradArgs& a, char* lds, int
                                                     (p * C::KG + ks * 2) * C::SA * 16);
     }
   };
-  using S = WSched<C::CA, C::CB, P, C::NB>;
+  using S = WSched<C::CA, C::CB, P, C::NB, C::KS * C::PS, C::KS, NT + P * MT>;
+  constexpr S sched{};
+  static_assert(sched.begin[C::KS * C::PS] == S::kItems, "an item has no place");
 
   __syncthreads();   // the previous segment's waves are done with the LDS
   {
-    const Rsrc R = next_stage(), R1 = next_stage();
+    auto load = [&](Raw& x) {
+      const Rsrc R = next_stage();
 #pragma unroll
-    for (int r = 0; r < 8; ++r) load_a(R, r);
+      for (int r = 0; r < 8; ++r) load_a(x, R, r);
 #pragma unroll
-    for (int r = 0; r < 9; ++r) load_b(R, r);
+      for (int r = 0; r < 9; ++r) load_b(x, R, r);
+    };
+    load(raw[0]);
+    if constexpr (SETS == 2) load(raw[1]);
 #pragma unroll
-    for (int c = 0; c < C::CA; ++c) conv_a(c, 0);
+    for (int c = 0; c < C::CA; ++c) {
+      conv_a(raw[0], c, -1);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) load_a(R1, r);
+      for (int p = 0; p < P; ++p) put_a(c, p, 0);
+    }
 #pragma unroll
-    for (int c = 0; c < C::CB; ++c) conv_b(c, 0);
+    for (int h = 0; h < 2; ++h) scale_b(raw[0], h);
 #pragma unroll
-    for (int r = 0; r < 9; ++r) load_b(R1, r);
+    for (int c = 0; c < C::CB / 2; ++c) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) conv_b(raw[0], c, q);
+      put_b(c, 0, 0);
+      put_b(c, 1, 0);
+    }
+    load(raw[0]);
   }
   __syncthreads();
   Frags F[2];
 #pragma unroll
   for (int k = 0; k < NT + P * MT; ++k) read_frag(F[0], 0, 0, k);
-  int base = 0;
-  for (int st = s_a; st < s_b; ++st) {
-    const int nbase = base ^ C::kStage;
+  // stage in buffer `base` (0 or kStage): its products; the next stage from
+  // x to the other buffer; the one after next but one from memory to x
+  auto stage = [&](Raw& x, auto BASE) {
+    constexpr int base = decltype(BASE)::value, nbase = base ^ C::kStage;
     const Rsrc R = next_stage();
-static_for<0, C::KS>([&](auto KSC) {
+    static_for<0, C::KS>([&](auto KSC) {
       constexpr int ks = decltype(KSC)::value;
       constexpr bool last = ks == C::KS - 1;
       if constexpr (last) {
@@ -371,21 +472,37 @@ static_for<0, C::KS>([&](auto KSC) {
         __syncthreads();
       }
       static_for<0, C::PS>([&](auto QC) {
-        constexpr int q = decltype(QC)::value, p = q / (MT * NT), x = q / NT % MT, y = q % NT, n = ks * C::PS + q;
-        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(F[ks & 1].a[p][x], F[ks & 1].b[y], acc[x][y], 0, 0, 0);
+        constexpr int q = decltype(QC)::value, p = q / (MT * NT), xt = q / NT % MT, y = q % NT, n = ks * C::PS + q;
+        acc[xt][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(F[ks & 1].a[p][xt], F[ks & 1].b[y], acc[xt][y], 0, 0, 0);
         read_frag(F[(ks + 1) & 1], last ? nbase : base, last ? 0 : ks + 1, q);
-        static_for<S::first(n), S::first(n + 1)>([&](auto KC) {
-          constexpr int k = decltype(KC)::value;
-          if constexpr (k < C::CA) conv_a(k, nbase);
-          else if constexpr (k < C::CA + 8) load_a(R, k - C::CA);
-          else if constexpr (k < C::CA + 8 + C::CB) conv_b(k - C::CA - 8, nbase);
-          else load_b(R, k - C::CA - 8 - C::CB);
+        static_for<sched.begin[n], sched.begin[n + 1]>([&](auto KC) {
+          constexpr int k = sched.order[decltype(KC)::value];
+          if constexpr (k < S::kA) {
+            constexpr int c = k / S::kPerA, part = k % S::kPerA;
+            if constexpr (part < S::kParts) conv_a(x, c, S::kParts == 1 ? -1 : part);
+            else put_a(c, part - S::kParts, nbase);
+          } else if constexpr (k < S::kA + 2) {
+            scale_b(x, k - S::kA);
+          } else if constexpr (k < S::kCols) {
+            constexpr int c = (k - S::kA - 2) / 6, part = (k - S::kA - 2) % 6;
+            if constexpr (part < 4) conv_b(x, c, part);
+            else put_b(c, part - 4, nbase);
+          } else if constexpr (k < S::kCols + 8) {
+            load_a(x, R, k - S::kCols);
+          } else {
+            load_b(x, R, k - S::kCols - 8);
+          }
         });
         __builtin_amdgcn_sched_barrier(0);
       });
     });
-    base = nbase;
+  };
+  int st = s_a;
+  for (; st + 1 < s_b; st += 2) {
+    stage(raw[SETS - 1], std::integral_constant<int, 0>{});
+    stage(raw[0], std::integral_constant<int, C::kStage>{});
   }
+  if (st < s_b) stage(raw[SETS - 1], std::integral_constant<int, 0>{});
 
   // Register e of MFMA tile (x, y) is element (8 (e / 4) + 4 (lane / 32) + e %
   // 4, lane % 32) of the 32 x 32 outputs.  One path for W and for a segment
@@ -395,93 +512,105 @@ static_for<0, C::KS>([&](auto KSC) {
   const int mi = part ? C::SA : a.m - i0, nj = part ? C::SB : a.d - j0;
   const float alpha = part ? 1.f : a.alpha;
   const bool add = !part && a.accumulate;
+  int elane = threadIdx.x & 63;
+  asm volatile("" : "+v"(elane));
   // the sums stay in the accumulator registers until their own turn
   auto hold = [](wf32x16& v) {
     if constexpr (MT * NT > 4) asm volatile("" : "+a"(v));
   };
+  const int r0 = 32 * wm * MT + 4 * (elane >> 5), c0 = 32 * wn * NT + (elane & 31);
 #pragma unroll
   for (int x = 0; x < MT; ++x)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int i = wgrad_row(32 * (wm * MT + x) + 8 * (e / 4) + 4 * (lane >> 5) + e % 4, C::CA, mi);
-      float* row = out + (int64_t)i * ldo;
+      const int i = wgrad_row(r0 + 32 * x + 8 * (e / 4) + e % 4, C::CA, mi);
+      float* row = out + (int64_t)i * ldo + c0;
 #pragma unroll
       for (int y = 0; y < NT; ++y) {
-        const int j = 32 * (wn * NT + y) + (lane & 31);
         hold(acc[x][y]);
         float v = alpha * acc[x][y][e];
-        if (i >= 0 && j < nj) {
-          if (add) v += row[j];
-          row[j] = v;
+        if (i >= 0 && c0 + 32 * y < nj) {
+          if (add) v += row[32 * y];
+          row[32 * y] = v;
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-// Workgroup g (consecutive numbers on one die) first takes whole tiles in
-// rounds; the tiles left over, fewer than there are workgroups, are cut into
-// equal contiguous ranges of (tile, stage).  A range that is not a whole tile
-// goes to part, segment number g + tile, and k_wgrad_join adds the segments
-// of a tile in order: no atomics, the same sums every time.
+// One workgroup's pieces (WLevel).  Workgroups of one die have consecutive
+// numbers.  A piece that is not a whole tile goes to part at its number, and
+// k_wgrad_join adds the pieces of a tile in token order: no atomics, the same
+// sums every time.
 template <typename TD, int FMT, int MT, int NT, int KT>
 __global__ void __launch_bounds__(256, MT * NT > 4 ? 1 : 2) k_wgrad(WgradArgs a) {
   using C = WTile<TD, FMT, MT, NT, KT>;
   __shared__ __attribute__((aligned(16))) char lds[C::kLds];
   const int G = gridDim.x;
-  const int g = G % 8 == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
-  const int whole = a.rounds * G, tiles = a.nbm * a.nbn;
-  const int64_t U = (int64_t)(tiles - whole) * a.nst;
-  const int64_t u0 = U * g / G, u1 = U * (g + 1) / G;
-  // the range: its first tile and stage, its stages (divisions run on the
-  // vector units: the compiler is told that the results are uniform)
-  int left = __builtin_amdgcn_readfirstlane((int)(u0 / a.nst));
-  int s_a = __builtin_amdgcn_readfirstlane((int)(u0 % a.nst));
-  int n = __builtin_amdgcn_readfirstlane((int)(u1 - u0));
-  for (int rd = 0; rd < a.rounds || n > 0; ++rd) {
-    const bool full = rd < a.rounds;
-    const int tile = full ? rd * G + g : whole + left;
-    const int s0 = full ? 0 : s_a, s1 = full || n >= a.nst - s_a ? a.nst : s_a + n;
-    const bool split = s0 > 0 || s1 < a.nst;
+  int g = G % 8 == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+  // (divisions run on the vector units: the compiler is told that the results are uniform)
+  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  auto piece = [&](int tile, int from, int units, int number) {
     int ti, tj;
     wgrad_tile(tile, a.nbm, a.nbn, ti, tj);
-    wgrad_segment<TD, FMT, MT, NT, KT>(a, lds, __builtin_amdgcn_readfirstlane(ti), __builtin_amdgcn_readfirstlane(tj),
-                                       s0, s1, split ? a.part + (int64_t)(g + left) * C::SA * C::SB : nullptr);
-    if (!full) {
-      n -= s1 - s0;
-      s_a = 0;
-      ++left;
+    const int s0 = from * a.unit;
+    const int s1 = s0 + units * a.unit < a.nst ? s0 + units * a.unit : a.nst;
+    const bool whole = s0 == 0 && s1 == a.nst;
+    wgrad_segment<TD, FMT, MT, NT, KT>(a, lds, uniform(ti), uniform(tj), uniform(s0), uniform(s1),
+                                       whole ? nullptr : a.part + (int64_t)uniform(number) * C::SA * C::SB);
+  };
+  int k = 0;
+  for (WLevel v = wgrad_levels(a.nbm * a.nbn, (a.nst + a.unit - 1) / a.unit, G); !v.done();) {
+    int tile, from = v.from, units = v.n, number;
+    if (v.split()) {
+      const int mine = v.count() * v.R;
+      if (g >= mine) {
+        g -= mine;
+        v.next();
+        continue;
+      }
+      const int c = g / v.R;
+      tile = g - c * v.R;
+      from += c * v.C;
+      units = v.C;
+      number = v.base + g;
+      v.R = 0;   // the last piece
+    } else {
+      tile = g + k * v.W;
+      number = v.base + tile;
+      if (k == v.count() || tile >= v.R) {
+        k = 0;
+        v.next();
+        continue;
+      }
+      ++k;
     }
+    piece(uniform(v.tile0 + tile), from, units, number);
   }
 }
 
-// W of the split tiles from their segments, added in token order.  Each
+// W of the split tiles from their pieces, added in token order.  Each
 // workgroup takes 1024 elements of one tile, four a thread.
 template <int MT, int NT>
-__global__ void __launch_bounds__(256) k_wgrad_join(WgradArgs a, int G, int ca) {
+__global__ void __launch_bounds__(256) k_wgrad_join(WgradArgs a, int G, int first, int ca) {
   constexpr int SA = 64 * MT, SB = 64 * NT, PER = MT * NT * 4;   // workgroups of a tile
-  const int left = blockIdx.x / PER, q = blockIdx.x % PER;
-  const int whole = a.rounds * G, tiles = a.nbm * a.nbn;
-  const int64_t U = (int64_t)(tiles - whole) * a.nst;
-  // workgroups whose ranges meet [left nst, (left + 1) nst): first holds its start, last its end
-  const int64_t b = (int64_t)left * a.nst, e = b + a.nst;
-  int first = (int)(b * G / U), last = (int)((e - 1) * G / U);
-  while (U * (first + 1) / G <= b) ++first;
-  while (U * (last + 1) / G < e) ++last;
-  if (first == last) return;   // written by its workgroup
+  const int tile = first + blockIdx.x / PER, q = blockIdx.x % PER;
   const int f = (q * 256 + threadIdx.x) * 4;
-  const float* p = a.part + (int64_t)(first + left) * SA * SB + f;
-  float4 s = *reinterpret_cast<const float4*>(p);
-  for (int k = first + 1; k <= last; ++k) {
-    p += SA * SB;
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+  float4 s = {0.f, 0.f, 0.f, 0.f};
+  for (WLevel v = wgrad_levels(a.nbm * a.nbn, (a.nst + a.unit - 1) / a.unit, G); !v.done(); v.next()) {
+    const int r = tile - v.tile0;
+    const int count = v.split() ? v.count() : v.from > 0 && r < v.tiles() ? 1 : 0;
+    for (int c = 0; c < count; ++c) {
+      const float4 x = *reinterpret_cast<const float4*>(a.part + ((int64_t)v.base + (int64_t)c * v.R + r) * SA * SB + f);
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    if (!v.split() && r < v.tiles()) break;
   }
   int ti, tj;
-  wgrad_tile(whole + left, a.nbm, a.nbn, ti, tj);
+  wgrad_tile(tile, a.nbm, a.nbn, ti, tj);
   const int i = wgrad_row(f / SB, ca, a.m - ti * SA), j = tj * SB + f % SB;
   if (i < 0) return;
   float* w = a.W + (int64_t)(ti * SA + i) * a.ldw + j;
@@ -566,29 +695,54 @@ namespace {
 
 struct WgradPlan {
   int variant;         // 0: vector units, 1: 256 x 256 tiles, 2: 128 x 128
-  int kt, side, nbm, nbn, nst, rounds, grid;
-  int64_t split;       // tiles cut into segments
+  int kt, side, nbm, nbn, nst, unit, grid;
+  int first, split;    // first split tile, split tiles
   size_t bytes;
 };
 
-WgradPlan wgrad_plan(int64_t T, int m, int d, int dtype, int64_t ldd, int64_t ldc) {
-  WgradPlan p{};
-  const int size = dtype == GIFT_FP32 ? 4 : 2;
-  if (m < 8 || 64 * ldd * size >= ((int64_t)1 << 31) || 64 * ldc >= ((int64_t)1 << 31) || T == 0) return p;
-  p.variant = cdiv(m, 256) * cdiv(d, 256) >= 32 ? 1 : 2;
-  p.side = p.variant == 1 ? 256 : 128;
-  p.kt = p.variant == 1 && dtype != GIFT_BF16 ? 32 : 64;
+// A plan with tiles of `side`, and what it is expected to take (us): the
+// stages of a workgroup, W written once, and for split tiles the launch that
+// joins them and their pieces written and read.  Per 64 tokens a workgroup
+// takes (measured at 1536 x 6144, 16384 tokens; bf16, fp16, fp32 delta):
+//   256 x 256  1.3, 3.8, 5.4      one workgroup a compute unit
+//   128 x 128  1.3, 1.3, 1.8      bf16: two workgroups a compute unit
+double wgrad_try(WgradPlan& p, int variant, bool split, int64_t T, int m, int d, int dtype) {
+  static const double kStage[2][3] = {{1.6, 3.8, 5.4}, {1.3, 1.3, 1.8}};
+  const int t = dtype == GIFT_BF16 ? 0 : dtype == GIFT_FP16 ? 1 : 2;
+  p.variant = variant;
+  p.side = variant == 1 ? 256 : 128;
+  p.kt = variant == 1 && dtype != GIFT_BF16 ? 32 : 64;
   p.nbm = (int)cdiv(m, p.side);
   p.nbn = (int)cdiv(d, p.side);
   p.nst = (int)cdiv(T, p.kt);
-  const int64_t tiles = (int64_t)p.nbm * p.nbn;
-  const int G = kWgradGroups;
-  const int64_t units = tiles * p.nst;
-  p.grid = (int)(units < G ? units : G);
-  p.rounds = (int)(tiles / p.grid);
-  p.split = tiles - (int64_t)p.rounds * p.grid;
-  p.bytes = p.split ? (size_t)(p.split + p.grid) * p.side * p.side * 4 : 0;
-  return p;
+  p.grid = variant == 2 && dtype == GIFT_BF16 ? 2 * kWgradGroups : kWgradGroups;
+  p.unit = split ? 128 / p.kt : p.nst;
+  WLevel v = wgrad_levels(p.nbm * p.nbn, (int)cdiv(p.nst, p.unit), p.grid);
+  const double stages = (double)v.C * p.unit * p.kt / 64;
+  if (!v.split()) v.next();   // whole tiles
+  p.first = v.tile0;
+  p.split = v.from == 0 && v.n == v.C ? 0 : v.R;
+  int pieces = 0;
+  for (; !v.done(); v.next()) pieces = v.base + (v.split() ? v.count() * v.R : v.tiles());
+  p.bytes = p.split ? (size_t)pieces * p.side * p.side * 4 : 0;
+  return stages * kStage[variant - 1][t] + (p.split ? 5.0 + 2.0 * (double)p.bytes / 4.5e6 : 0.0);
+}
+
+WgradPlan wgrad_plan(int64_t T, int m, int d, int dtype, int64_t ldd, int64_t ldc) {
+  WgradPlan best{};
+  const int size = dtype == GIFT_FP32 ? 4 : 2;
+  if (m < 8 || 64 * ldd * size >= ((int64_t)1 << 31) || 64 * ldc >= ((int64_t)1 << 31) || T == 0) return best;
+  double least = 0;
+  for (int variant = 1; variant <= 2; ++variant)
+    for (int split = 0; split < 2; ++split) {
+      WgradPlan p{};
+      const double t = wgrad_try(p, variant, split != 0, T, m, d, dtype);
+      if (best.variant == 0 || t < least) {
+        best = p;
+        least = t;
+      }
+    }
+  return best;
 }
 
 template <typename TD, int FMT, int MT, int KT>
@@ -596,7 +750,7 @@ void wgrad_go(const WgradArgs& a, const WgradPlan& p, hipStream_t s) {
   hipLaunchKernelGGL((k_wgrad<TD, FMT, MT, MT, KT>), dim3((unsigned)p.grid), dim3(256), 0, s, a);
   if (p.split)
     hipLaunchKernelGGL((k_wgrad_join<MT, MT>), dim3((unsigned)(p.split * MT * MT * 4)), dim3(256), 0, s, a, p.grid,
-                       KT * MT / 32);
+                       p.first, KT * MT / 32);
 }
 
 template <typename TD, int KT>
@@ -645,7 +799,7 @@ hipError_t launch_weight_grad(const WgradCall& c, hipStream_t s) {
   a.nst = p.nst;
   a.nbm = p.nbm;
   a.nbn = p.nbn;
-  a.rounds = p.rounds;
+  a.unit = p.unit;
   if (c.dtype == GIFT_BF16) wgrad_t<Bf16, 64>(a, p, s);
   else if (c.dtype == GIFT_FP16) wgrad_t<Fp16, 32>(a, p, s);
   else wgrad_t<float, 32>(a, p, s);
