@@ -556,25 +556,32 @@ class Group:
 # allocator's pool of the stream they launch on, so it may be dropped as soon
 # as the call returns; tensors the caller passes are the caller's to order.
 
+# Small calls cost what the host does (a launch is about 4 us, a current_stream
+# object 3, an allocation 2), so these wrappers do each thing once.
+
 def _rows(t, what, T=None, n=None, dtype=None):
     """Checks a [T][n] tensor with unit column stride; returns its leading dimension."""
-    if t.dim() != 2 or t.dtype not in DTYPES or (dtype is not None and t.dtype != dtype):
+    dt, shape = t.dtype, t.shape
+    if dt not in DTYPES or len(shape) != 2 or (dtype is not None and dt != dtype):
         raise ValueError(f"{what} must be a [T][n] tensor of {dtype or 'bf16, fp16 or fp32'}")
-    if (T is not None and t.shape[0] != T) or (n is not None and t.shape[1] != n):
-        raise ValueError(f"{what} must have shape [{T}][{n}], not {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = shape
+    if (T is not None and rows != T) or (n is not None and cols != n):
+        raise ValueError(f"{what} must have shape [{T}][{n}], not {tuple(shape)}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{what} must have unit column stride")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on the GPU")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return ld if rows > 1 else max(cols, 1)
 
 
 def _vector(t, what, n, dtypes, device):
+    """Checks a dense vector; returns its address (None for None)."""
     if t is None:
         return None
-    if t.numel() != n or t.dim() != 1 or t.dtype not in dtypes or (n > 1 and t.stride(0) != 1) or t.device != device:
+    if t.shape != (n,) or t.dtype not in dtypes or (n > 1 and t.stride(0) != 1) or t.device != device:
         raise ValueError(f"{what} must be a dense vector of {n} {' or '.join(map(str, dtypes))} on {device}")
-    return t
+    return t.data_ptr()
 
 
 def _empty(stream, shape, dtype, device):
@@ -582,6 +589,24 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_like(stream, t):
+    """A dense tensor of t's shape and type."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)      # a little quicker than torch.empty
+    return _empty(stream, t.shape, t.dtype, t.device)
+
+
+def _raw_stream(stream):
+    """Handle of the stream, or of the current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+_F32 = (torch.float32,)
+_WEIGHTS = {t: (t, torch.float32) for t in DTYPES}
 
 
 class ActCheckpoint:
@@ -599,12 +624,14 @@ class ActCheckpoint:
         nb, groups = -(-self.d // 32), -(-self.T // 8)
         if codes is None:
             codes = _empty(stream, (self.T, nb * 32), torch.uint8, device)
+        elif codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[0] != self.T or (
+                codes.shape[1] < nb * 32) or codes.stride(1) != 1:
+            raise ValueError(f"codes must be a uint8 [{self.T}][>= {nb * 32}] tensor on the GPU with unit column stride")
+        if not codes.is_cuda:
+            raise ValueError("a checkpoint must be on the GPU")
         if bscales is None:
             bscales = _empty(stream, (groups, nb, 8), torch.uint8, codes.device)
-        if codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[0] != self.T or codes.shape[1] < nb * 32 or (
-                codes.stride(1) != 1) or not codes.is_cuda:
-            raise ValueError(f"codes must be a uint8 [{self.T}][>= {nb * 32}] tensor on the GPU with unit column stride")
-        if bscales.dtype != torch.uint8 or bscales.numel() != groups * nb * 8 or not bscales.is_contiguous() or (
+        elif bscales.dtype != torch.uint8 or bscales.numel() != groups * nb * 8 or not bscales.is_contiguous() or (
                 bscales.device != codes.device):
             raise ValueError(f"bscales must be a contiguous uint8 [{groups}][{nb}][8] tensor beside the codes")
         self.codes, self.bscales, self.device = codes, bscales, codes.device
@@ -617,16 +644,17 @@ class ActCheckpoint:
 
     def save(self, x: torch.Tensor, stream=None):
         ld = _rows(x, "x", self.T, self.d)
-        _check(_lib.gift_act_save(x.data_ptr(), DTYPES[x.dtype], ld, self.T, self.d, self._ref, _stream(stream)),
+        _check(_lib.gift_act_save(x.data_ptr(), DTYPES[x.dtype], ld, self.T, self.d, self._ref, _raw_stream(stream)),
                "gift_act_save")
         return self
 
     def restore(self, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
         if out is None:
-            out = _empty(stream, (self.T, self.d), dtype, self.device)
-        ld = _rows(out, "out", self.T, self.d)
+            out, ld = _empty(stream, (self.T, self.d), dtype, self.device), self.d
+        else:
+            ld = _rows(out, "out", self.T, self.d)
         _check(_lib.gift_act_restore(self._ref, self.T, self.d, out.data_ptr(), DTYPES[out.dtype], ld,
-                                     _stream(stream)), "gift_act_restore")
+                                     _raw_stream(stream)), "gift_act_restore")
         return out
 
 
@@ -638,19 +666,20 @@ def norm_forward(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, kin
     weight and bias: of x's type or both fp32."""
     kind = NORMS.get(kind, kind)
     ld = _rows(x, "x")
-    (T, d), dev = x.shape, x.device
-    wt = weight.dtype if weight is not None else bias.dtype if bias is not None else x.dtype
-    _vector(weight, "weight", d, (x.dtype, torch.float32), dev)
-    _vector(bias, "bias", d, (wt,), dev)
+    (T, d), dev, dt = x.shape, x.device, x.dtype
+    wt = weight.dtype if weight is not None else bias.dtype if bias is not None else dt
+    wp, bp = _vector(weight, "weight", d, _WEIGHTS[dt], dev), _vector(bias, "bias", d, (wt,), dev)
     if ckpt is not None and (ckpt.T, ckpt.d) != (T, d):
         raise ValueError("the checkpoint has another shape than x")
-    y = _empty(stream, (T, d), x.dtype, dev) if out is None else out
-    ldy = _rows(y, "out", T, d, x.dtype)
+    if out is None:
+        y, ldy = _empty_like(stream, x), d
+    else:
+        y, ldy = out, _rows(out, "out", T, d, dt)
     mean = _empty(stream, (T,), torch.float32, dev) if kind == NORM_LAYER else None
     rstd = _empty(stream, (T,), torch.float32, dev)
-    _check(_lib.gift_norm_forward(kind, x.data_ptr(), DTYPES[x.dtype], ld, T, d, _ptr(weight), _ptr(bias), DTYPES[wt],
-                                  eps, y.data_ptr(), ldy, _ptr(mean), rstd.data_ptr(),
-                                  None if ckpt is None else ckpt._ref, _stream(stream)), "gift_norm_forward")
+    _check(_lib.gift_norm_forward(kind, x.data_ptr(), DTYPES[dt], ld, T, d, wp, bp, DTYPES[wt], eps, y.data_ptr(), ldy,
+                                  None if mean is None else mean.data_ptr(), rstd.data_ptr(),
+                                  None if ckpt is None else ckpt._ref, _raw_stream(stream)), "gift_norm_forward")
     return y, mean, rstd
 
 
@@ -661,36 +690,42 @@ def norm_backward(dy: torch.Tensor, x, mean, rstd, weight=None, kind="layer", dx
     "rms" unless given).  accumulate: added to the given dweight and dbias."""
     kind = NORMS.get(kind, kind)
     ld = _rows(dy, "dy")
-    (T, d), dev = dy.shape, dy.device
+    (T, d), dev, dt = dy.shape, dy.device, dy.dtype
     ck = x if isinstance(x, ActCheckpoint) else None
     if ck is not None:
         if (ck.T, ck.d) != (T, d):
             raise ValueError("the checkpoint has another shape than dy")
         ldx, xp = 0, None
     else:
-        ldx, xp = _rows(x, "x", T, d, dy.dtype), x.data_ptr()
-    _vector(weight, "weight", d, (dy.dtype, torch.float32), dev)
-    _vector(mean, "mean", T, (torch.float32,), dev)
-    _vector(rstd, "rstd", T, (torch.float32,), dev)
+        ldx, xp = _rows(x, "x", T, d, dt), x.data_ptr()
+    wp = _vector(weight, "weight", d, _WEIGHTS[dt], dev)
+    mp, rp = _vector(mean, "mean", T, _F32, dev), _vector(rstd, "rstd", T, _F32, dev)
     if accumulate and dweight is None and dbias is None:
         raise ValueError("accumulate needs the gradients to add to")
-    if not accumulate:
-        if dweight is None:
-            dweight = _empty(stream, (d,), torch.float32, dev)
-        if dbias is None and kind == NORM_LAYER:
-            dbias = _empty(stream, (d,), torch.float32, dev)
-    _vector(dweight, "dweight", d, (torch.float32,), dev)
-    _vector(dbias, "dbias", d, (torch.float32,), dev)
+    if dweight is not None:
+        dwp = _vector(dweight, "dweight", d, _F32, dev)
+    elif not accumulate:
+        dweight = _empty(stream, (d,), torch.float32, dev)
+        dwp = dweight.data_ptr()
+    else:
+        dwp = None
+    if dbias is not None:
+        dbp = _vector(dbias, "dbias", d, _F32, dev)
+    elif not accumulate and kind == NORM_LAYER:
+        dbias = _empty(stream, (d,), torch.float32, dev)
+        dbp = dbias.data_ptr()
+    else:
+        dbp = None
     if dx is None:
-        dx = _empty(stream, (T, d), dy.dtype, dev)
-    lddx = _rows(dx, "dx", T, d, dy.dtype)
+        dx, lddx = _empty_like(stream, dy), d
+    else:
+        lddx = _rows(dx, "dx", T, d, dt)
     if work is None:
-        work = _empty(stream, (int(_lib.gift_norm_workspace_bytes(T, d)),), torch.uint8, dev)
-    wt = dy.dtype if weight is None else weight.dtype
-    _check(_lib.gift_norm_backward(kind, dy.data_ptr(), DTYPES[dy.dtype], ld, xp, ldx, None if ck is None else ck._ref,
-                                   T, d, _ptr(weight), DTYPES[wt], _ptr(mean), _ptr(rstd), dx.data_ptr(), lddx,
-                                   _ptr(dweight), _ptr(dbias), int(accumulate), work.data_ptr(), work.numel(),
-                                   _stream(stream)), "gift_norm_backward")
+        work = _empty(stream, (_lib.gift_norm_workspace_bytes(T, d),), torch.uint8, dev)
+    _check(_lib.gift_norm_backward(kind, dy.data_ptr(), DTYPES[dt], ld, xp, ldx, None if ck is None else ck._ref,
+                                   T, d, wp, DTYPES[dt if weight is None else weight.dtype], mp, rp, dx.data_ptr(),
+                                   lddx, dwp, dbp, int(accumulate), work.data_ptr(), work.numel(),
+                                   _raw_stream(stream)), "gift_norm_backward")
     return dx, dweight, dbias
 
 
@@ -701,15 +736,15 @@ def weight_grad(delta: torch.Tensor, ckpt: ActCheckpoint, alpha: float = 1.0, ou
     [T][d]: the gradient Layer.encode takes."""
     T, d = ckpt.T, ckpt.d
     ld = _rows(delta, "delta", T)
-    m, dev = delta.shape[1], delta.device
+    m, dev, dt = delta.shape[1], delta.device, DTYPES[delta.dtype]
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the tensor to add to")
-        out = _empty(stream, (m, d), torch.float32, dev)
-    ldw = _rows(out, "out", m, d, torch.float32)
-    dt = DTYPES[delta.dtype]
+        out, ldw = _empty(stream, (m, d), torch.float32, dev), d
+    else:
+        ldw = _rows(out, "out", m, d, torch.float32)
     if work is None:
-        work = _empty(stream, (int(_lib.gift_weight_grad_workspace_bytes(T, m, d, dt)),), torch.uint8, dev)
+        work = _empty(stream, (_lib.gift_weight_grad_workspace_bytes(T, m, d, dt),), torch.uint8, dev)
     _check(_lib.gift_weight_grad(delta.data_ptr(), dt, ld, m, ckpt._ref, T, d, alpha, int(accumulate), out.data_ptr(),
-                                 ldw, work.data_ptr(), work.numel(), _stream(stream)), "gift_weight_grad")
+                                 ldw, work.data_ptr(), work.numel(), _raw_stream(stream)), "gift_weight_grad")
     return out

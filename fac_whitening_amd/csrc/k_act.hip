@@ -35,9 +35,12 @@ struct ActArgs {
   int64_t T;
   int d, nb, fmt, lxlog;
   int colblocks;      // workgroups across a row
+  int stream;         // restore: the output is larger than the caches (act8.hpp)
 };
 
-template <typename TX>
+// STREAM: codes larger than the caches (act8.hpp), the input is read past them
+// too (16384 x 6144 bf16: 55.7 -> 51 us).
+template <typename TX, bool STREAM>
 __global__ void __launch_bounds__(kActThreads) k_act_save(ActArgs a) {
   const int lx = 1 << a.lxlog;
   const int cx = threadIdx.x & (lx - 1), ty = threadIdx.x >> a.lxlog;
@@ -51,7 +54,7 @@ __global__ void __launch_bounds__(kActThreads) k_act_save(ActArgs a) {
   const int n = a.d - col;   // elements of this chunk inside the row (may be <= 0 or > 8)
   Raw8<TX> r[kActGroup];
 #pragma unroll
-  for (int i = 0; i < kActGroup; ++i) r[i] = load8(x + (t0 + i) * a.ld + col, t0 + i < a.T ? n : 0);
+  for (int i = 0; i < kActGroup; ++i) r[i] = load8<TX, STREAM>(x + (t0 + i) * a.ld + col, t0 + i < a.T ? n : 0);
   uint32_t ex[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < kActGroup; ++i) {
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(kActThreads) k_act_save(ActArgs a) {
     ex[i / 4] |= e << (8 * (i % 4));
     uint32_t w[2];
     act_encode8(v, e, a.fmt, w);
-    if (t0 + i < a.T) __builtin_memcpy(__builtin_assume_aligned(a.codes + (t0 + i) * a.ldc + col, 8), w, 8);
+    if (t0 + i < a.T) store_words<2>(a.codes + (t0 + i) * a.ldc + col, w, STREAM);
   }
   if ((cx & 3) == 0)
     __builtin_memcpy(__builtin_assume_aligned(a.bscales + (g * a.nb + col / kActBlock) * kActGroup, 8), ex, 8);
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(kActThreads) k_act_restore(ActArgs a) {
     act_decode8(w[i], (ex[i / 4] >> (8 * (i % 4))) & 0xFFu, a.fmt, v);
     Raw8<TX> r;
     pack8(v, r);
-    if (t0 + i < a.T) store8(out + (t0 + i) * a.ld + col, r, n);
+    if (t0 + i < a.T) store8(out + (t0 + i) * a.ld + col, r, n, a.stream != 0);
   }
 }
 
@@ -132,9 +135,14 @@ hipError_t launch_act_save(const void* x, int dtype, int64_t ld, int64_t T, int 
   a.x = x;
   a.ld = ld;
   const dim3 gd((unsigned)grid), bd(kActThreads);
-  if (dtype == GIFT_BF16) hipLaunchKernelGGL(k_act_save<Bf16>, gd, bd, 0, s, a);
-  else if (dtype == GIFT_FP16) hipLaunchKernelGGL(k_act_save<Fp16>, gd, bd, 0, s, a);
-  else hipLaunchKernelGGL(k_act_save<float>, gd, bd, 0, s, a);
+  auto go = [&](auto tx) {
+    using TX = decltype(tx);
+    if (T * a.nb * kActBlock > kStreamBytes) hipLaunchKernelGGL((k_act_save<TX, true>), gd, bd, 0, s, a);
+    else hipLaunchKernelGGL((k_act_save<TX, false>), gd, bd, 0, s, a);
+  };
+  if (dtype == GIFT_BF16) go(Bf16{});
+  else if (dtype == GIFT_FP16) go(Fp16{});
+  else go(float{});
   return hipGetLastError();
 }
 
@@ -145,6 +153,7 @@ hipError_t launch_act_restore(const gift_act_ckpt& c, int64_t T, int d, void* ou
   ActArgs a = act_args(c, T, d, &grid);
   a.out = out;
   a.ld = ld;
+  a.stream = T * d * (dtype == GIFT_FP32 ? 4 : 2) > kStreamBytes;
   const dim3 gd((unsigned)grid), bd(kActThreads);
   if (dtype == GIFT_BF16) hipLaunchKernelGGL(k_act_restore<Bf16>, gd, bd, 0, s, a);
   else if (dtype == GIFT_FP16) hipLaunchKernelGGL(k_act_restore<Fp16>, gd, bd, 0, s, a);

@@ -44,7 +44,9 @@ struct NormArgs {
   int64_t ldy;
   const void* dy;
   int64_t lddy;
-  float* part;          // backward: [P][2][d] partial sums of dgamma, dbeta (NULL: not wanted)
+  float* part;          // backward: [P][sums][d] partial sums of dgamma, dbeta (NULL: not wanted)
+  int sums;             // 2, or 1: dgamma alone
+  int stream;           // the output is larger than the caches (act8.hpp)
   int64_t groups;       // backward: row groups (kNormRows<G> rows each)
 };
 
@@ -52,7 +54,7 @@ namespace {
 
 template <int G>
 constexpr int kNormThreads = G > 256 ? G : 256;
-// Rows per step of a workgroup, and per group of 8 (16 for G = 16) rows whose
+// Rows of a row group of the backward pass: one or two groups of 8 rows whose
 // exponents share cache lines.
 template <int G>
 constexpr int kNormRows = G == 16 ? 16 : 8;
@@ -125,107 +127,93 @@ __device__ __forceinline__ void chunk_values(const RowChunk<T, true>& c, const N
 
 }  // namespace
 
-// Forward.  R rows per group of lanes at once (their loads are in flight
-// together); a workgroup covers 8 rows (16 for G = 16), or one row when G is
-// the whole workgroup.  In that last case consecutive workgroups go to
-// different dies (round robin over 8); the row map below gives the 8 rows of
-// one exponent group to one die, so their bytes merge in one L2.
+// Forward, one row per lane group (two rows at once, for more loads in
+// flight, took the registers of a third wave per SIMD: 32.7 against 29.4 us
+// with a checkpoint, 20.8 against 19.8 without, at 16384 x 1536 bf16).
+// Where a row takes a whole workgroup, consecutive workgroups go to different
+// dies (round robin over 8); the row map below gives the 8 rows of one
+// exponent group to one die, so their bytes merge in one L2.
 template <typename T, int G, int CH>
 __global__ void __launch_bounds__(kNormThreads<G>) k_norm_fwd(NormArgs a) {
-  constexpr int NT = kNormThreads<G>;
-  constexpr int S = NT / G;                                 // rows of a step
-  constexpr int R = G > 64 ? 1 : kNormRows<G> / S;          // rows per lane group
   __shared__ float red[2][2][8];
   int flip = 0;
-  const int lane = threadIdx.x % G, sub = threadIdx.x / G;
-  int64_t row0;
+  const int lane = threadIdx.x % G;
+  int64_t t;
   if constexpr (G > 64) {
     const int64_t b = blockIdx.x;
-    row0 = (b & ~(int64_t)63) + (b & 7) * 8 + ((b >> 3) & 7);
-    if (row0 >= a.T) return;
+    t = (b & ~(int64_t)63) + (b & 7) * 8 + ((b >> 3) & 7);
   } else {
-    row0 = (int64_t)blockIdx.x * kNormRows<G> + sub * R;
-    if (row0 >= a.T) return;   // per wave or part of a wave; no barriers below for these G
+    t = (int64_t)blockIdx.x * (kNormThreads<G> / G) + threadIdx.x / G;
   }
-  Raw8<T> raw[R][CH];
+  if (t >= a.T) return;   // the lanes of a row together (G <= 64 has no barriers below)
+  Raw8<T> raw[CH];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = (c * G + lane) * 8;
-      raw[r][c] = load8(static_cast<const T*>(a.x) + (row0 + r) * a.ldx + col, row0 + r < a.T ? a.d - col : 0);
-    }
-  float mean[R], rstd[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    mean[r] = 0.f;
-    if (a.layer) {
-      float s = 0.f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        float v[8];
-        unpack8(raw[r][c], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s += v[j];
-      }
-      row_sums<G, 1>(&s, red, flip);
-      mean[r] = s / (float)a.d;   // correctly rounded: a constant row is centred exactly
-    }
-    float q = 0.f;
+  for (int c = 0; c < CH; ++c) {
+    const int col = (c * G + lane) * 8;
+    raw[c] = load8(static_cast<const T*>(a.x) + t * a.ldx + col, a.d - col);
+  }
+  float mean = 0.f;
+  if (a.layer) {
+    float s = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int n = a.d - (c * G + lane) * 8;
       float v[8];
-      unpack8(raw[r][c], v);
+      unpack8(raw[c], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = j < n ? v[j] - mean[r] : 0.f;
-        q += u * u;
-      }
+      for (int j = 0; j < 8; ++j) s += v[j];
     }
-    row_sums<G, 1>(&q, red, flip);
-    rstd[r] = 1.0f / sqrtf(q / (float)a.d + a.eps);
-    if (lane == 0 && row0 + r < a.T) {
-      if (a.mean) a.mean[row0 + r] = mean[r];
-      if (a.rstd) a.rstd[row0 + r] = rstd[r];
+    row_sums<G, 1>(&s, red, flip);
+    mean = s / (float)a.d;   // correctly rounded: a constant row is centred exactly
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int n = a.d - (c * G + lane) * 8;
+    float v[8];
+    unpack8(raw[c], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float u = j < n ? v[j] - mean : 0.f;
+      q += u * u;
     }
+  }
+  row_sums<G, 1>(&q, red, flip);
+  const float rstd = 1.0f / sqrtf(q / (float)a.d + a.eps);
+  if (lane == 0) {
+    if (a.mean) a.mean[t] = mean;
+    if (a.rstd) a.rstd[t] = rstd;
   }
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int col = (c * G + lane) * 8;
     const int n = a.d - col;
-    float w[8], b[8];
+    float w[8], b[8], v[8], y[8];
     if (a.w) load_weights<T>(a.w, a.w32, col, n, w);
     if (a.b) load_weights<T>(a.b, a.w32, col, n, b);
+    unpack8(raw[c], v);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t t = row0 + r;
-      float v[8], y[8];
-      unpack8(raw[r][c], v);
+    for (int j = 0; j < 8; ++j) {
+      y[j] = (v[j] - mean) * rstd;
+      if (a.w) y[j] *= w[j];
+      if (a.b) y[j] += b[j];
+    }
+    Raw8<T> o;
+    pack8(y, o);
+    store8(static_cast<T*>(a.y) + t * a.ldy + col, o, n, a.stream != 0);
+    if (a.codes) {
+      uint32_t m = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        y[j] = (v[j] - mean[r]) * rstd[r];
-        if (a.w) y[j] *= w[j];
-        if (a.b) y[j] += b[j];
+        const uint32_t u = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+        m = u > m ? u : m;
       }
-      Raw8<T> o;
-      pack8(y, o);
-      if (t < a.T) store8(static_cast<T*>(a.y) + t * a.ldy + col, o, n);
-      if (a.codes) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t u = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-          m = u > m ? u : m;
-        }
-        const uint32_t e = act_exponent(quad_max(m), a.fmt);
-        uint32_t k[2];
-        act_encode8(v, e, a.fmt, k);
-        if (t < a.T && col < a.nb * kActBlock) {
-          __builtin_memcpy(__builtin_assume_aligned(a.codes + t * a.ldc + col, 8), k, 8);
-          if ((lane & 3) == 0)
-            a.bscales[((t >> 3) * a.nb + col / kActBlock) * kActGroup + (t & 7)] = (uint8_t)e;
-        }
+      const uint32_t e = act_exponent(quad_max(m), a.fmt);
+      uint32_t k[2];
+      act_encode8(v, e, a.fmt, k);
+      if (col < a.nb * kActBlock) {
+        __builtin_memcpy(__builtin_assume_aligned(a.codes + t * a.ldc + col, 8), k, 8);
+        if ((lane & 3) == 0)
+          a.bscales[((t >> 3) * a.nb + col / kActBlock) * kActGroup + (t & 7)] = (uint8_t)e;
       }
     }
   }
@@ -233,9 +221,15 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_fwd(NormArgs a) {
 
 // Backward.  Workgroup p takes the row groups p, p + P, ...; each lane keeps
 // the dgamma and dbeta sums of its own columns in registers over all of them
-// and fetches the next row while it works on the present one.  The partial
-// sums of the workgroups go to part [P][2][d] and are added in order by
-// k_norm_reduce: no atomics, the same result every time.
+// and has the next rows in flight while it works on the present one: two
+// (kAhead) where the registers of two resident workgroups allow it, one with
+// four chunks or three of fp32, none above 12288 columns (there the weights
+// come from the cache each time too).  The partial sums of the workgroups go
+// to part [P][sums][d] and are added in order by k_norm_reduce: no atomics,
+// the same result every time.
+template <typename T, int G, int CH>
+constexpr int kAhead = G == 512 && CH == 4 ? 0 : CH <= 2 || (CH == 3 && sizeof(T) == 2) ? 2 : 1;
+
 template <typename T, bool CK, int G, int CH>
 __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
   constexpr int NT = kNormThreads<G>;
@@ -244,10 +238,7 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
   __shared__ float comb[S > 1 ? S : 1][S > 1 ? G : 1][9];   // padded: 9 words a lane, no bank conflicts
   int flip = 0;
   const int lane = threadIdx.x % G, sub = threadIdx.x / G;
-  // Above 12288 columns neither the next row nor the weights fit the
-  // registers (256 a lane at 512 threads): there a row is fetched when its
-  // turn comes, and the weights come from the cache each time.
-  constexpr bool AHEAD = !(G == 512 && CH == 4);
+  constexpr int AHEAD = kAhead<T, G, CH>, BUF = AHEAD ? AHEAD : 1;
   float wk[AHEAD ? CH : 1][8], dg[CH][8], db[CH][8];
   auto weights = [&](int c, float* v) {
     const int col = (c * G + lane) * 8;
@@ -259,43 +250,45 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[c][j] = db[c][j] = 0.f;
-    if constexpr (AHEAD) weights(c, wk[c]);
+    if constexpr (AHEAD > 0) weights(c, wk[c]);
   }
-  RowChunk<T, CK> xr[CH];
-  Raw8<T> yr[CH];
-  float mean_n = 0.f, rstd_n = 0.f;
+  struct Row {
+    RowChunk<T, CK> x[CH];
+    Raw8<T> y[CH];
+    float mean, rstd;
+  };
+  Row rows[BUF];
   // step k of this workgroup: row group p + (k / STEPS) P, its rows k % STEPS
   const int64_t mine = a.groups > blockIdx.x ? cdiv(a.groups - blockIdx.x, gridDim.x) : 0;
   const int64_t steps = mine * STEPS;
   auto row_of = [&](int64_t k) {
     return ((int64_t)blockIdx.x + (k / STEPS) * gridDim.x) * RB + (k % STEPS) * S + sub;
   };
-  auto fetch = [&](int64_t k) {
+  auto fetch = [&](Row& b, int64_t k) {
     const int64_t t = row_of(k);
     const bool in = k < steps && t < a.T;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (c * G + lane) * 8;
-      load_chunk(xr[c], a, t, col, in ? a.d - col : 0);
-      yr[c] = load8(static_cast<const T*>(a.dy) + t * a.lddy + col, in ? a.d - col : 0);
+      load_chunk(b.x[c], a, t, col, in ? a.d - col : 0);
+      b.y[c] = load8(static_cast<const T*>(a.dy) + t * a.lddy + col, in ? a.d - col : 0);
     }
-    mean_n = in && a.layer ? a.mean[t] : 0.f;
-    rstd_n = in ? a.rstd[t] : 0.f;
+    b.mean = in && a.layer ? a.mean[t] : 0.f;
+    b.rstd = in ? a.rstd[t] : 0.f;
   };
-  if (AHEAD) fetch(0);
-  for (int64_t k = 0; k < steps; ++k) {
+  auto step = [&](Row& b, int64_t k) {
     const int64_t t = row_of(k);
-    if (!AHEAD) fetch(k);
-    const float mean = mean_n, rstd = rstd_n;
+    if constexpr (AHEAD == 0) fetch(b, k);
+    const float mean = b.mean, rstd = b.rstd;
     float xh[CH][8], t8[CH][8];
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int n = t < a.T ? a.d - (c * G + lane) * 8 : 0;
       float* w = wk[AHEAD ? c : 0];
-      if constexpr (!AHEAD) weights(c, w);
-      chunk_values(xr[c], a, xh[c]);
-      unpack8(yr[c], t8[c]);
+      if constexpr (AHEAD == 0) weights(c, w);
+      chunk_values(b.x[c], a, xh[c]);
+      unpack8(b.y[c], t8[c]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // columns past the row (and rows past T) add nothing: dy reads zero there
@@ -307,7 +300,7 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
         db[c][j] += t8[c][j];
       }
     }
-    if (AHEAD) fetch(k + 1);
+    if constexpr (AHEAD > 0) fetch(b, k + AHEAD);
     row_sums<G, 2>(s, red, flip);
     const float c1 = s[0] * a.invd, c2 = a.layer ? s[1] * a.invd : 0.f;
     if (t < a.T) {
@@ -315,23 +308,31 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
       for (int c = 0; c < CH; ++c) {
         const int col = (c * G + lane) * 8;
         float* w = wk[AHEAD ? c : 0];
-        if constexpr (!AHEAD) weights(c, w);
+        if constexpr (AHEAD == 0) weights(c, w);
         float o[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = rstd * (t8[c][j] * w[j] - c2 - xh[c][j] * c1);
         Raw8<T> r;
         pack8(o, r);
-        store8(static_cast<T*>(a.y) + t * a.ldy + col, r, a.d - col);
+        store8(static_cast<T*>(a.y) + t * a.ldy + col, r, a.d - col, a.stream != 0);
       }
     }
+  };
+#pragma unroll
+  for (int q = 0; q < AHEAD; ++q) fetch(rows[q], q);
+  for (int64_t k = 0; k < steps; k += BUF) {
+    step(rows[0], k);
+    if constexpr (BUF == 2)
+      if (k + 1 < steps) step(rows[1], k + 1);   // (the same for the whole workgroup)
   }
   if (!a.part) return;
   // this workgroup's sums: the S row slots are added through LDS in order
-  float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
+  float* part = a.part + (int64_t)blockIdx.x * a.sums * a.d;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
+      if (which == a.sums) break;
       float* v = which == 0 ? dg[c] : db[c];
       const int col = (c * G + lane) * 8;
       if constexpr (S > 1) {
@@ -351,25 +352,31 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
     }
 }
 
-// dgamma, dbeta [d] from part [P][2][d]: a workgroup adds 64 columns (32
-// threads down the partials for each), four sums in turn per thread, then
+// dgamma, dbeta [d] from part [P][sums][d]: a workgroup adds 32 columns, 32
+// threads down the partials of each (eight loads of a thread in flight), then
 // the threads' sums in order.  accumulate: added to what the outputs hold.
 constexpr int kReduceCols = 32, kReduceRows = 32;
 __global__ void __launch_bounds__(kReduceCols* kReduceRows) k_norm_reduce(const float* __restrict__ part, int P, int d,
-                                                                         float* __restrict__ dw, float* __restrict__ db,
-                                                                         int accumulate) {
+                                                                         int n, float* __restrict__ dw,
+                                                                         float* __restrict__ db, int accumulate) {
   __shared__ float sums[kReduceRows][kReduceCols + 1];
   const int cx = threadIdx.x % kReduceCols, ry = threadIdx.x / kReduceCols;
-  const int j = blockIdx.x * kReduceCols + cx;   // column of [2][d]
+  const int j = blockIdx.x * kReduceCols + cx;   // column of [sums][d], n in all
   float v = 0.f;
-  if (j < 2 * d)
-    for (int p = ry; p < P; p += kReduceRows) v += part[(int64_t)p * 2 * d + j];
+  for (int p = ry; p < P; p += 8 * kReduceRows) {
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      x[q] = j < n && p + q * kReduceRows < P ? part[(int64_t)(p + q * kReduceRows) * n + j] : 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v += x[q];
+  }
   sums[ry][cx] = v;
   __syncthreads();
-  if (ry != 0 || j >= 2 * d) return;
+  if (ry != 0 || j >= n) return;
 #pragma unroll
   for (int q = 1; q < kReduceRows; ++q) v += sums[q][cx];
-  float* out = j < d ? (dw ? dw + j : nullptr) : (db ? db + (j - d) : nullptr);
+  float* out = j < d ? (dw ? dw + j : nullptr) : db + (j - d);
   if (out) *out = accumulate ? *out + v : v;
 }
 
@@ -398,11 +405,12 @@ void norm_variant(int d, F&& f) {
 
 int64_t norm_row_groups(int64_t T, int d) { return cdiv(T, d <= 128 ? 16 : 8); }
 
-// Workgroups of the backward pass: at most 512, two a compute unit (their partial
-// sums cost 16 d bytes each), never more than there are row groups.
+// Workgroups of the backward pass: as many as are resident (two of 256
+// threads a compute unit, one of 512; every further one adds 8 d bytes of
+// partial sums to write and read), never more than there are row groups.
 int norm_partials(int64_t T, int d) {
-  const int64_t g = norm_row_groups(T, d);
-  return (int)(g < 512 ? (g > 0 ? g : 1) : 512);
+  const int64_t g = norm_row_groups(T, d), most = d > 8192 ? 256 : 512;
+  return (int)(g < most ? (g > 0 ? g : 1) : most);
 }
 
 static NormArgs norm_args(const NormCall& c) {
@@ -430,12 +438,13 @@ static NormArgs norm_args(const NormCall& c) {
   a.ldy = c.ldy;
   a.dy = c.dy;
   a.lddy = c.lddy;
+  a.stream = c.T * c.d * (c.dtype == GIFT_FP32 ? 4 : 2) > kStreamBytes;
   return a;
 }
 
 // Workgroups of the forward: a row each above 2048 columns (whole sets of 64
-// for the row map), a row group each below.
-int64_t norm_forward_grid(int64_t T, int d) { return d > 2048 ? cdiv(T, 64) * 64 : norm_row_groups(T, d); }
+// for the row map), four or, up to 128 columns, sixteen rows each below.
+int64_t norm_forward_grid(int64_t T, int d) { return d > 2048 ? cdiv(T, 64) * 64 : cdiv(T, d <= 128 ? 16 : 4); }
 
 template <typename T>
 static void norm_fwd_t(const NormArgs& a, hipStream_t s) {
@@ -467,6 +476,7 @@ hipError_t launch_norm_backward(const NormCall& c, float* part, float* dw, float
   const int P = norm_partials(c.T, c.d);
   NormArgs a = norm_args(c);
   a.part = part;
+  a.sums = db ? 2 : 1;
   a.groups = norm_row_groups(c.T, c.d);
   if (c.ckpt) {
     if (c.dtype == GIFT_BF16) norm_bwd_t<Bf16, true>(a, P, s);
@@ -480,8 +490,8 @@ hipError_t launch_norm_backward(const NormCall& c, float* part, float* dw, float
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (part)
-    hipLaunchKernelGGL(k_norm_reduce, dim3((unsigned)cdiv(2 * (int64_t)c.d, kReduceCols)),
-                       dim3(kReduceCols * kReduceRows), 0, s, part, P, c.d, dw, db, accumulate);
+    hipLaunchKernelGGL(k_norm_reduce, dim3((unsigned)cdiv(a.sums * (int64_t)c.d, kReduceCols)),
+                       dim3(kReduceCols * kReduceRows), 0, s, part, P, c.d, a.sums * c.d, dw, db, accumulate);
   return hipGetLastError();
 }
 
