@@ -117,6 +117,30 @@ __device__ __forceinline__ void unpack8(const Raw8<float>& r, float* v) {
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
 }
 
+// Bits of the largest magnitude of the eight as fp32 (at or above 0x7F800000
+// when one is an infinity or NaN).  Magnitudes order like their bits, so a
+// 16-bit type compares two at a time.
+__device__ __forceinline__ uint32_t amax16(const uint32_t* w) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m = __builtin_bit_cast(u16x2, w[0] & 0x7FFF7FFFu);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
+  return m[0] > m[1] ? m[0] : m[1];
+}
+__device__ __forceinline__ uint32_t amax_bits(const Raw8<Bf16>& r) { return amax16(r.w) << 16; }
+__device__ __forceinline__ uint32_t amax_bits(const Raw8<Fp16>& r) {
+  return __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)amax16(r.w)));
+}
+__device__ __forceinline__ uint32_t amax_bits(const Raw8<float>& r) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = r.w[i] & 0x7FFFFFFFu;
+    m = b > m ? b : m;
+  }
+  return m;
+}
+
 // One rounding to nearest even each (none for fp32).
 __device__ __forceinline__ void pack8(const float* v, Raw8<Bf16>& r) {
 #pragma unroll

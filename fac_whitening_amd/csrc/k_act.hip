@@ -60,13 +60,7 @@ __global__ void __launch_bounds__(kActThreads) k_act_save(ActArgs a) {
   for (int i = 0; i < kActGroup; ++i) {
     float v[8];
     unpack8(r[i], v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-      m = b > m ? b : m;
-    }
-    const uint32_t e = act_exponent(quad_max(m), a.fmt);
+    const uint32_t e = act_exponent(quad_max(amax_bits(r[i])), a.fmt);
     ex[i / 4] |= e << (8 * (i % 4));
     uint32_t w[2];
     act_encode8(v, e, a.fmt, w);

@@ -84,6 +84,14 @@ __device__ __forceinline__ void row_sums(float* v, float (*red)[2][8], int& flip
   }
 }
 
+// A row's last chunk alone can be partial or empty (norm_variant takes the
+// fewest chunks): the others are loaded, counted and stored without checks,
+// which is a third of the instructions of these loops.
+template <int CH>
+__device__ __forceinline__ int chunk_size(int c, int n) {
+  return c < CH - 1 ? 8 : n;
+}
+
 // Eight weights at column col (n of them inside the row).
 template <typename T>
 __device__ __forceinline__ void load_weights(const void* p, int w32, int col, int n, float* v) {
@@ -147,33 +155,31 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_fwd(NormArgs a) {
   }
   if (t >= a.T) return;   // the lanes of a row together (G <= 64 has no barriers below)
   Raw8<T> raw[CH];
+  float v[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int col = (c * G + lane) * 8;
-    raw[c] = load8(static_cast<const T*>(a.x) + t * a.ldx + col, a.d - col);
+    raw[c] = load8(static_cast<const T*>(a.x) + t * a.ldx + col, chunk_size<CH>(c, a.d - col));
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    unpack8(raw[c], v[c]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += v[c][j];
   }
   float mean = 0.f;
   if (a.layer) {
-    float s = 0.f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float v[8];
-      unpack8(raw[c], v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[j];
-    }
     row_sums<G, 1>(&s, red, flip);
     mean = s / (float)a.d;   // correctly rounded: a constant row is centred exactly
   }
   float q = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int n = a.d - (c * G + lane) * 8;
-    float v[8];
-    unpack8(raw[c], v);
+    const int n = chunk_size<CH>(c, a.d - (c * G + lane) * 8);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float u = j < n ? v[j] - mean : 0.f;
+      const float u = j < n ? v[c][j] - mean : 0.f;
       q += u * u;
     }
   }
@@ -186,36 +192,29 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_fwd(NormArgs a) {
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int col = (c * G + lane) * 8;
-    const int n = a.d - col;
-    float w[8], b[8], v[8], y[8];
+    const int n = chunk_size<CH>(c, a.d - col);
+    if (a.codes) {
+      const uint32_t e = act_exponent(quad_max(amax_bits(raw[c])), a.fmt);
+      uint32_t k[2];
+      act_encode8(v[c], e, a.fmt, k);
+      if (c < CH - 1 || col < a.nb * kActBlock) {
+        __builtin_memcpy(__builtin_assume_aligned(a.codes + t * a.ldc + col, 8), k, 8);
+        if ((lane & 3) == 0)
+          a.bscales[((t >> 3) * a.nb + col / kActBlock) * kActGroup + (t & 7)] = (uint8_t)e;
+      }
+    }
+    float w[8], b[8], y[8];
     if (a.w) load_weights<T>(a.w, a.w32, col, n, w);
     if (a.b) load_weights<T>(a.b, a.w32, col, n, b);
-    unpack8(raw[c], v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      y[j] = (v[j] - mean) * rstd;
+      y[j] = (v[c][j] - mean) * rstd;
       if (a.w) y[j] *= w[j];
       if (a.b) y[j] += b[j];
     }
     Raw8<T> o;
     pack8(y, o);
     store8(static_cast<T*>(a.y) + t * a.ldy + col, o, n, a.stream != 0);
-    if (a.codes) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t u = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-        m = u > m ? u : m;
-      }
-      const uint32_t e = act_exponent(quad_max(m), a.fmt);
-      uint32_t k[2];
-      act_encode8(v, e, a.fmt, k);
-      if (col < a.nb * kActBlock) {
-        __builtin_memcpy(__builtin_assume_aligned(a.codes + t * a.ldc + col, 8), k, 8);
-        if ((lane & 3) == 0)
-          a.bscales[((t >> 3) * a.nb + col / kActBlock) * kActGroup + (t & 7)] = (uint8_t)e;
-      }
-    }
   }
 }
 
@@ -237,14 +236,14 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
   __shared__ float red[2][2][8];
   __shared__ float comb[S > 1 ? S : 1][S > 1 ? G : 1][9];   // padded: 9 words a lane, no bank conflicts
   int flip = 0;
-  const int lane = threadIdx.x % G, sub = threadIdx.x / G;
+  const int lane = threadIdx.x % G, sub = S > 1 ? threadIdx.x / G : 0;
   constexpr int AHEAD = kAhead<T, G, CH>, BUF = AHEAD ? AHEAD : 1;
   float wk[AHEAD ? CH : 1][8], dg[CH][8], db[CH][8];
   auto weights = [&](int c, float* v) {
     const int col = (c * G + lane) * 8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 1.f;
-    if (a.w) load_weights<T>(a.w, a.w32, col, a.d - col, v);
+    if (a.w) load_weights<T>(a.w, a.w32, col, chunk_size<CH>(c, a.d - col), v);
   };
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -266,56 +265,60 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
   };
   auto fetch = [&](Row& b, int64_t k) {
     const int64_t t = row_of(k);
-    const bool in = k < steps && t < a.T;
+    if (k < steps && t < a.T) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = (c * G + lane) * 8;
-      load_chunk(b.x[c], a, t, col, in ? a.d - col : 0);
-      b.y[c] = load8(static_cast<const T*>(a.dy) + t * a.lddy + col, in ? a.d - col : 0);
+      for (int c = 0; c < CH; ++c) {
+        const int col = (c * G + lane) * 8, n = chunk_size<CH>(c, a.d - col);
+        load_chunk(b.x[c], a, t, col, n);
+        b.y[c] = load8(static_cast<const T*>(a.dy) + t * a.lddy + col, n);
+      }
+      b.mean = a.layer ? a.mean[t] : 0.f;
+      b.rstd = a.rstd[t];
     }
-    b.mean = in && a.layer ? a.mean[t] : 0.f;
-    b.rstd = in ? a.rstd[t] : 0.f;
   };
   auto step = [&](Row& b, int64_t k) {
     const int64_t t = row_of(k);
+    if (t >= a.T) return;   // the lanes of a row together (all of the workgroup where row_sums has a barrier)
     if constexpr (AHEAD == 0) fetch(b, k);
     const float mean = b.mean, rstd = b.rstd;
     float xh[CH][8], t8[CH][8];
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int n = t < a.T ? a.d - (c * G + lane) * 8 : 0;
+      const int n = chunk_size<CH>(c, a.d - (c * G + lane) * 8);
       float* w = wk[AHEAD ? c : 0];
       if constexpr (AHEAD == 0) weights(c, w);
       chunk_values(b.x[c], a, xh[c]);
       unpack8(b.y[c], t8[c]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        // columns past the row (and rows past T) add nothing: dy reads zero there
+        // columns past the row add nothing, dy reads zero there
         xh[c][j] = j < n ? (xh[c][j] - mean) * rstd : 0.f;
-        const float g = t8[c][j] * w[j];
-        s[0] += g * xh[c][j];
-        s[1] += g;
+        s[0] += t8[c][j] * w[j] * xh[c][j];
         dg[c][j] += t8[c][j] * xh[c][j];
-        db[c][j] += t8[c][j];
+      }
+      if (a.layer || a.sums == 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s[1] += t8[c][j] * w[j];
+          db[c][j] += t8[c][j];
+        }
       }
     }
     if constexpr (AHEAD > 0) fetch(b, k + AHEAD);
     row_sums<G, 2>(s, red, flip);
     const float c1 = s[0] * a.invd, c2 = a.layer ? s[1] * a.invd : 0.f;
-    if (t < a.T) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int col = (c * G + lane) * 8;
-        float* w = wk[AHEAD ? c : 0];
-        if constexpr (AHEAD == 0) weights(c, w);
-        float o[8];
+    for (int c = 0; c < CH; ++c) {
+      const int col = (c * G + lane) * 8;
+      float* w = wk[AHEAD ? c : 0];
+      if constexpr (AHEAD == 0) weights(c, w);
+      float o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = rstd * (t8[c][j] * w[j] - c2 - xh[c][j] * c1);
-        Raw8<T> r;
-        pack8(o, r);
-        store8(static_cast<T*>(a.y) + t * a.ldy + col, r, a.d - col, a.stream != 0);
-      }
+      for (int j = 0; j < 8; ++j) o[j] = rstd * (t8[c][j] * w[j] - c2 - xh[c][j] * c1);
+      Raw8<T> r;
+      pack8(o, r);
+      store8(static_cast<T*>(a.y) + t * a.ldy + col, r, chunk_size<CH>(c, a.d - col), a.stream != 0);
     }
   };
 #pragma unroll
