@@ -149,6 +149,7 @@ gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, in
   if (!d_W || !aligned(d_W, 4) || ldw < d) return GIFT_ERR_INVALID_ARG;
   if (!d_work || !aligned(d_work, 16)) return GIFT_ERR_INVALID_ARG;
   if (work_bytes < gift_weight_grad_workspace_bytes(T, m, d, dtype)) return GIFT_ERR_WORKSPACE;
+  if (gift::cdiv(m, 64) * gift::cdiv(d, 64) > kMaxGrid) return GIFT_ERR_UNSUPPORTED;
   gift::WgradCall c{};
   c.delta = d_delta;
   c.dtype = dtype;

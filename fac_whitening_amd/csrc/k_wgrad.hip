@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "act8.hpp"
+#include "wgrad_levels.hpp"
 
 namespace gift {
 
@@ -29,55 +30,6 @@ struct WgradArgs {
   int nbm, nbn;            // output tiles down and across
   int unit;                // stages of a unit: tiles are split at whole units
 };
-
-// How G workgroups share R tiles of n units each: in levels, each a set of
-// pieces of one length that start at one place of the token axis, so that
-// workgroups on one die walk the same tokens at the same time and share them
-// through its L2.  With C = ceil(R n / G) units for every workgroup:
-//   n >= C: q = n / C workgroups a tile take C units each and are done
-//   n <  C: every workgroup takes all n units of C / n tiles
-// and what is left of tiles, units, workgroups and C goes through the same
-// step again (the Euclidean algorithm on n and C).  Pieces of a level are
-// numbered from `base`; piece 0 .. R - 1 of a level is that of its tile.
-struct WLevel {
-  int R, n, W, C;      // tiles, units left of each, workgroups, units left for each
-  int from;            // first unit of the pieces
-  int tile0;           // first tile
-  int base;            // number of the level's first piece
-  __host__ __device__ bool done() const { return R == 0 || n == 0; }
-  __host__ __device__ bool split() const { return n >= C; }            // pieces of C units, count() a tile
-  __host__ __device__ int count() const { return split() ? n / C : C / n; }
-  __host__ __device__ int tiles() const {                              // tiles that are finished at this level
-    const int64_t t = split() ? R : (int64_t)count() * W;
-    return t < R ? (int)t : R;
-  }
-  __host__ __device__ void next() {
-    if (split()) {
-      const int q = n / C;
-      base += q * R;
-      W -= q * R;
-      from += q * C;
-      n -= q * C;
-    } else {
-      const int t = tiles();
-      base += t;
-      C -= count() * n;
-      R -= t;
-      tile0 += t;
-    }
-  }
-};
-
-// The first level.  Pieces of whole tiles are written to W directly and have
-// no number.
-__host__ __device__ inline WLevel wgrad_levels(int tiles, int units, int G) {
-  WLevel v{};
-  v.R = tiles;
-  v.n = units;
-  v.W = G;
-  v.C = (int)(((int64_t)tiles * units + G - 1) / G);
-  return v;
-}
 
 __device__ __forceinline__ float elem_f32(const float* p) { return *p; }
 __device__ __forceinline__ float elem_f32(const Bf16* p) { return __uint_as_float((uint32_t)p->v << 16); }
@@ -550,43 +502,16 @@ __global__ void __launch_bounds__(256, MT * NT > 4 ? 1 : 2) k_wgrad(WgradArgs a)
   int g = G % 8 == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
   // (divisions run on the vector units: the compiler is told that the results are uniform)
   auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-  auto piece = [&](int tile, int from, int units, int number) {
-    int ti, tj;
-    wgrad_tile(tile, a.nbm, a.nbn, ti, tj);
-    const int s0 = from * a.unit;
-    const int s1 = s0 + units * a.unit < a.nst ? s0 + units * a.unit : a.nst;
-    const bool whole = s0 == 0 && s1 == a.nst;
-    wgrad_segment<TD, FMT, MT, NT, KT>(a, lds, uniform(ti), uniform(tj), uniform(s0), uniform(s1),
-                                       whole ? nullptr : a.part + (int64_t)uniform(number) * C::SA * C::SB);
-  };
-  int k = 0;
-  for (WLevel v = wgrad_levels(a.nbm * a.nbn, (a.nst + a.unit - 1) / a.unit, G); !v.done();) {
-    int tile, from = v.from, units = v.n, number;
-    if (v.split()) {
-      const int mine = v.count() * v.R;
-      if (g >= mine) {
-        g -= mine;
-        v.next();
-        continue;
-      }
-      const int c = g / v.R;
-      tile = g - c * v.R;
-      from += c * v.C;
-      units = v.C;
-      number = v.base + g;
-      v.R = 0;   // the last piece
-    } else {
-      tile = g + k * v.W;
-      number = v.base + tile;
-      if (k == v.count() || tile >= v.R) {
-        k = 0;
-        v.next();
-        continue;
-      }
-      ++k;
-    }
-    piece(uniform(v.tile0 + tile), from, units, number);
-  }
+  wgrad_walk(wgrad_levels(a.nbm * a.nbn, (a.nst + a.unit - 1) / a.unit, G), g, uniform,
+             [&](int tile, int from, int units, int number) {
+               int ti, tj;
+               wgrad_tile(tile, a.nbm, a.nbn, ti, tj);
+               const int s0 = from * a.unit;
+               const int s1 = s0 + units * a.unit < a.nst ? s0 + units * a.unit : a.nst;
+               const bool whole = s0 == 0 && s1 == a.nst;
+               wgrad_segment<TD, FMT, MT, NT, KT>(a, lds, uniform(ti), uniform(tj), s0, s1,
+                                                  whole ? nullptr : a.part + (int64_t)number * C::SA * C::SB);
+             });
 }
 
 // W of the split tiles from their pieces, added in token order.  Each
@@ -597,18 +522,13 @@ __global__ void __launch_bounds__(256) k_wgrad_join(WgradArgs a, int G, int firs
   const int tile = first + blockIdx.x / PER, q = blockIdx.x % PER;
   const int f = (q * 256 + threadIdx.x) * 4;
   float4 s = {0.f, 0.f, 0.f, 0.f};
-  for (WLevel v = wgrad_levels(a.nbm * a.nbn, (a.nst + a.unit - 1) / a.unit, G); !v.done(); v.next()) {
-    const int r = tile - v.tile0;
-    const int count = v.split() ? v.count() : v.from > 0 && r < v.tiles() ? 1 : 0;
-    for (int c = 0; c < count; ++c) {
-      const float4 x = *reinterpret_cast<const float4*>(a.part + ((int64_t)v.base + (int64_t)c * v.R + r) * SA * SB + f);
-      s.x += x.x;
-      s.y += x.y;
-      s.z += x.z;
-      s.w += x.w;
-    }
-    if (!v.split() && r < v.tiles()) break;
-  }
+  wgrad_pieces(wgrad_levels(a.nbm * a.nbn, (a.nst + a.unit - 1) / a.unit, G), tile, [&](int number) {
+    const float4 x = *reinterpret_cast<const float4*>(a.part + (int64_t)number * SA * SB + f);
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  });
   int ti, tj;
   wgrad_tile(tile, a.nbm, a.nbn, ti, tj);
   const int i = wgrad_row(f / SB, ca, a.m - ti * SA), j = tj * SB + f % SB;
@@ -623,6 +543,7 @@ __global__ void __launch_bounds__(256) k_wgrad_join(WgradArgs a, int G, int firs
     }
 }
 
+// Vector-unit form, for what the matrix-core form leaves out (see wgrad_plan):
 // 64 x 64 outputs per workgroup, 32 tokens per LDS stage, 4 x 4 outputs per
 // thread, fp32 products and sums over 256 tokens, folded into fp64.
 template <typename TD>
@@ -717,21 +638,23 @@ double wgrad_try(WgradPlan& p, int variant, bool split, int64_t T, int m, int d,
   p.nst = (int)cdiv(T, p.kt);
   p.grid = variant == 2 && dtype == GIFT_BF16 ? 2 * kWgradGroups : kWgradGroups;
   p.unit = split ? 128 / p.kt : p.nst;
-  WLevel v = wgrad_levels(p.nbm * p.nbn, (int)cdiv(p.nst, p.unit), p.grid);
+  const WLevel v = wgrad_levels(p.nbm * p.nbn, (int)cdiv(p.nst, p.unit), p.grid);
   const double stages = (double)v.C * p.unit * p.kt / 64;
-  if (!v.split()) v.next();   // whole tiles
-  p.first = v.tile0;
-  p.split = v.from == 0 && v.n == v.C ? 0 : v.R;
-  int pieces = 0;
-  for (; !v.done(); v.next()) pieces = v.base + (v.split() ? v.count() * v.R : v.tiles());
-  p.bytes = p.split ? (size_t)pieces * p.side * p.side * 4 : 0;
+  const WSplit w = wgrad_split(v);
+  p.first = w.first;
+  p.split = w.tiles;
+  p.bytes = (size_t)w.pieces * p.side * p.side * 4;
   return stages * kStage[variant - 1][t] + (p.split ? 5.0 + 2.0 * (double)p.bytes / 4.5e6 : 0.0);
 }
 
 WgradPlan wgrad_plan(int64_t T, int m, int d, int dtype, int64_t ldd, int64_t ldc) {
   WgradPlan best{};
   const int size = dtype == GIFT_FP32 ? 4 : 2;
-  if (m < 8 || 64 * ldd * size >= ((int64_t)1 << 31) || 64 * ldc >= ((int64_t)1 << 31) || T == 0) return best;
+  // The matrix-core form reads chunks of eight columns of delta, its buffer
+  // offsets within a stage are 32 bits, and so are its counts of tiles and
+  // stages; what is beyond runs on the vector units.
+  if (m < 8 || T == 0 || ldd >= ((int64_t)1 << 31) / (64 * size) || ldc >= ((int64_t)1 << 31) / 64) return best;
+  if (T >= (int64_t)1 << 34 || cdiv(m, 128) * cdiv(d, 128) * cdiv(T, 64) >= (int64_t)1 << 38) return best;
   double least = 0;
   for (int variant = 1; variant <= 2; ++variant)
     for (int split = 0; split < 2; ++split) {

@@ -480,7 +480,11 @@ gift_status gift_norm_backward(int32_t kind, const void* d_dy, int32_t dtype, in
 /* W [m][ldw] = alpha delta^T a (+ W when accumulate != 0), delta [T][ldd] of
  * type `dtype`, a [T][d] the values of the checkpoint.  delta enters the products
  * without loss (an fp32 value as the sum of three bf16 numbers, an fp16 value of two), a is
- * exact in bf16, sums are fp32. */
+ * exact in bf16, sums are fp32, added in the same order on every call.  d_work:
+ * gift_weight_grad_workspace_bytes, 16-byte aligned, free to be used again by
+ * what follows on the stream (partial sums of output tiles whose tokens are
+ * split over workgroups).  m < 8, or rows of delta or codes 2^25 bytes or more
+ * apart, run on the vector units, far more slowly. */
 size_t gift_weight_grad_workspace_bytes(int64_t T, int32_t m, int32_t d, int32_t dtype);
 gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, int32_t m, const gift_act_ckpt* h_ckpt,
                              int64_t T, int32_t d, float alpha, int32_t accumulate, float* d_W, int64_t ldw,
