@@ -522,12 +522,23 @@ __global__ void __launch_bounds__(256) k_wgrad_join(WgradArgs a, int G, int firs
   const int tile = first + blockIdx.x / PER, q = blockIdx.x % PER;
   const int f = (q * 256 + threadIdx.x) * 4;
   float4 s = {0.f, 0.f, 0.f, 0.f};
-  wgrad_pieces(wgrad_levels(a.nbm * a.nbn, (a.nst + a.unit - 1) / a.unit, G), tile, [&](int number) {
-    const float4 x = *reinterpret_cast<const float4*>(a.part + (int64_t)number * SA * SB + f);
-    s.x += x.x;
-    s.y += x.y;
-    s.z += x.z;
-    s.w += x.w;
+  wgrad_pieces(wgrad_levels(a.nbm * a.nbn, (a.nst + a.unit - 1) / a.unit, G), tile, [&](int number, int stride, int count) {
+    for (int c = 0; c < count; c += 8) {   // eight loads in flight
+      float4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k] = float4{0.f, 0.f, 0.f, 0.f};
+        if (c + k < count)
+          x[k] = *reinterpret_cast<const float4*>(a.part + ((int64_t)number + (int64_t)(c + k) * stride) * SA * SB + f);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s.x += x[k].x;
+        s.y += x[k].y;
+        s.z += x[k].z;
+        s.w += x[k].w;
+      }
+    }
   });
   int ti, tj;
   wgrad_tile(tile, a.nbm, a.nbn, ti, tj);
@@ -621,13 +632,14 @@ struct WgradPlan {
   size_t bytes;
 };
 
-// A plan with tiles of `side`, and what it is expected to take (us): the
-// stages of a workgroup, W written once, and for split tiles the launch that
-// joins them and their pieces written and read.  Per 64 tokens a workgroup
-// takes (measured at 1536 x 6144, 16384 tokens; bf16, fp16, fp32 delta):
-//   256 x 256  1.3, 3.8, 5.4      one workgroup a compute unit
-//   128 x 128  1.3, 1.3, 1.8      bf16: two workgroups a compute unit
-double wgrad_try(WgradPlan& p, int variant, bool split, int64_t T, int m, int d, int dtype) {
+// A plan with tiles of `side`, split at multiples of `units` x 64 tokens (0:
+// not split), and what it is expected to take (us): the stages of a
+// workgroup, and for split tiles the launch that joins them and their pieces
+// written and read.  Per 64 tokens a workgroup takes (measured; bf16, fp16,
+// fp32 delta):
+//   256 x 256  1.6, 3.8, 5.4      one workgroup a compute unit
+//   128 x 128  1.3, 1.3, 1.8      bf16: two workgroups a compute unit, 0.9 where there are no more than units
+double wgrad_try(WgradPlan& p, int variant, int units, int64_t T, int m, int d, int dtype) {
   static const double kStage[2][3] = {{1.6, 3.8, 5.4}, {1.3, 1.3, 1.8}};
   const int t = dtype == GIFT_BF16 ? 0 : dtype == GIFT_FP16 ? 1 : 2;
   p.variant = variant;
@@ -637,14 +649,16 @@ double wgrad_try(WgradPlan& p, int variant, bool split, int64_t T, int m, int d,
   p.nbn = (int)cdiv(d, p.side);
   p.nst = (int)cdiv(T, p.kt);
   p.grid = variant == 2 && dtype == GIFT_BF16 ? 2 * kWgradGroups : kWgradGroups;
-  p.unit = split ? 128 / p.kt : p.nst;
+  p.unit = units ? units * 64 / p.kt : p.nst;
   const WLevel v = wgrad_levels(p.nbm * p.nbn, (int)cdiv(p.nst, p.unit), p.grid);
   const double stages = (double)v.C * p.unit * p.kt / 64;
   const WSplit w = wgrad_split(v);
   p.first = w.first;
   p.split = w.tiles;
   p.bytes = (size_t)w.pieces * p.side * p.side * 4;
-  return stages * kStage[variant - 1][t] + (p.split ? 5.0 + 2.0 * (double)p.bytes / 4.5e6 : 0.0);
+  const bool alone = (int64_t)p.nbm * p.nbn * cdiv(p.nst, p.unit) <= (int64_t)kWgradGroups * v.C;
+  const double stage = variant == 2 && t == 0 && alone ? 0.9 : kStage[variant - 1][t];
+  return stages * stage + (p.split ? 5.0 + 2.0 * (double)p.bytes / 4.5e6 : 0.0);
 }
 
 WgradPlan wgrad_plan(int64_t T, int m, int d, int dtype, int64_t ldd, int64_t ldc) {
@@ -657,9 +671,9 @@ WgradPlan wgrad_plan(int64_t T, int m, int d, int dtype, int64_t ldd, int64_t ld
   if (T >= (int64_t)1 << 34 || cdiv(m, 128) * cdiv(d, 128) * cdiv(T, 64) >= (int64_t)1 << 38) return best;
   double least = 0;
   for (int variant = 1; variant <= 2; ++variant)
-    for (int split = 0; split < 2; ++split) {
+    for (int units = 0; units <= 2; ++units) {
       WgradPlan p{};
-      const double t = wgrad_try(p, variant, split != 0, T, m, d, dtype);
+      const double t = wgrad_try(p, variant, units, T, m, d, dtype);
       if (best.variant == 0 || t < least) {
         best = p;
         least = t;

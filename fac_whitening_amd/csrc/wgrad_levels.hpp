@@ -90,13 +90,14 @@ __host__ __device__ inline void wgrad_walk(WLevel v, int g, U&& uniform, F&& pie
   }
 }
 
-// Calls add(number) for the numbered pieces of a split tile in token order.
+// Calls add(number, stride, count) for each level's numbered pieces of a split
+// tile, in token order: number, number + stride, ...
 template <typename F>
 __host__ __device__ inline void wgrad_pieces(WLevel v, int tile, F&& add) {
   for (; !v.done(); v.next()) {
     const int r = tile - v.tile0;
     const int count = v.split() ? v.count() : v.from > 0 && r < v.tiles() ? 1 : 0;
-    for (int c = 0; c < count; ++c) add(v.base + c * v.R + r);
+    if (count) add(v.base + r, v.R, count);
     if (!v.split() && r < v.tiles()) break;
   }
 }

@@ -42,7 +42,9 @@ static bool check(int tiles, int units, int G) {
     std::sort(of[t].begin(), of[t].end());
     std::vector<int> want, got;
     for (auto& p : of[t]) want.push_back(p[2]);
-    if (t >= s.first && t < s.first + s.tiles) wgrad_pieces(v, t, [&](int number) { got.push_back(number); });
+    if (t >= s.first && t < s.first + s.tiles) wgrad_pieces(v, t, [&](int number, int stride, int count) {
+      for (int c = 0; c < count; ++c) got.push_back(number + c * stride);
+    });
     good = got == want;
   }
   if (!good) std::printf("fault: %d tiles of %d units over %d workgroups\n", tiles, units, G);
