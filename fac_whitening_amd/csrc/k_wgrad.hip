@@ -457,13 +457,7 @@ __device__ __forceinline__ void wgrad_segment(const WgradArgs& a, char* lds, int
   if (st < s_b) stage(raw[SETS - 1], std::integral_constant<int, 0>{});
 
   // Register e of MFMA tile (x, y) is element (8 (e / 4) + 4 (lane / 32) + e %
-  // 4, lane % 32) of the 32 x 32 outputs.  One path for W and for a segment
-  // (a whole [SA][SB] tile): two would keep copies of all sums.
-  float* out = part ? part : a.W + (int64_t)i0 * a.ldw + j0;
-  const int64_t ldo = part ? C::SB : a.ldw;
-  const int mi = part ? C::SA : a.m - i0, nj = part ? C::SB : a.d - j0;
-  const float alpha = part ? 1.f : a.alpha;
-  const bool add = !part && a.accumulate;
+  // 4, lane % 32) of the 32 x 32 outputs.
   int elane = threadIdx.x & 63;
   asm volatile("" : "+v"(elane));
   // the sums stay in the accumulator registers until their own turn
@@ -471,19 +465,38 @@ __device__ __forceinline__ void wgrad_segment(const WgradArgs& a, char* lds, int
     if constexpr (MT * NT > 4) asm volatile("" : "+a"(v));
   };
   const int r0 = 32 * wm * MT + 4 * (elane >> 5), c0 = 32 * wn * NT + (elane & 31);
+  if (part) {
+    // a piece, in the order of the registers: [wave][x][y][e / 4][lane][e % 4]
+    float* p = part + (int64_t)wave * MT * NT * 1024 + elane * 4;
+#pragma unroll
+    for (int x = 0; x < MT; ++x)
+#pragma unroll
+      for (int y = 0; y < NT; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          hold(acc[x][y]);
+          const float4 v = {acc[x][y][4 * e], acc[x][y][4 * e + 1], acc[x][y][4 * e + 2], acc[x][y][4 * e + 3]};
+          *reinterpret_cast<float4*>(p + ((x * NT + y) * 4 + e) * 256) = v;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    return;
+  }
+  float* out = a.W + (int64_t)i0 * a.ldw + j0;
+  const int mi = a.m - i0, nj = a.d - j0;
 #pragma unroll
   for (int x = 0; x < MT; ++x)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int i = wgrad_row(r0 + 32 * x + 8 * (e / 4) + e % 4, C::CA, mi);
-      float* row = out + (int64_t)i * ldo + c0;
+      const int i = wgrad_row(32 * (wm * MT + x) + 8 * (e / 4) + 4 * (elane >> 5) + e % 4, C::CA, mi);
+      float* row = out + (int64_t)i * a.ldw;
 #pragma unroll
       for (int y = 0; y < NT; ++y) {
+        const int j = 32 * (wn * NT + y) + (elane & 31);
         hold(acc[x][y]);
-        float v = alpha * acc[x][y][e];
-        if (i >= 0 && c0 + 32 * y < nj) {
-          if (add) v += row[32 * y];
-          row[32 * y] = v;
+        float v = a.alpha * acc[x][y][e];
+        if (i >= 0 && j < nj) {
+          if (a.accumulate) v += row[j];
+          row[j] = v;
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -542,16 +555,20 @@ __global__ void __launch_bounds__(256) k_wgrad_join(WgradArgs a, int G, int firs
   });
   int ti, tj;
   wgrad_tile(tile, a.nbm, a.nbn, ti, tj);
-  const int i = wgrad_row(f / SB, ca, a.m - ti * SA), j = tj * SB + f % SB;
-  if (i < 0) return;
-  float* w = a.W + (int64_t)(ti * SA + i) * a.ldw + j;
+  // this thread's four outputs (see the end of wgrad_segment)
+  const int lane = (f >> 2) & 63, e = (f >> 8) & 3, t = f >> 10;
+  const int y = t % NT, x = t / NT % MT, wave = t / (NT * MT);
+  const int j = tj * SB + 32 * ((wave & 1) * NT + y) + (lane & 31);
+  if (j >= a.d) return;
   const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (j + r < a.d) {
-      const float o = a.alpha * v[r];
-      w[r] = a.accumulate ? w[r] + o : o;
-    }
+  for (int r = 0; r < 4; ++r) {
+    const int i = wgrad_row(32 * ((wave >> 1) * MT + x) + 8 * e + 4 * (lane >> 5) + r, ca, a.m - ti * SA);
+    if (i < 0) continue;
+    float* w = a.W + (int64_t)(ti * SA + i) * a.ldw + j;
+    const float o = a.alpha * v[r];
+    *w = a.accumulate ? *w + o : o;
+  }
 }
 
 // Vector-unit form, for what the matrix-core form leaves out (see wgrad_plan):
