@@ -469,7 +469,8 @@ int norm_partials(int64_t T, int d) {
 
 // Up to this many rows the parameter gradients are made in the same launch,
 // by workgroups of their own that read x and dy once more (from the cache),
-// and the rows are spread over half the workgroups that are resident.  bf16, one launch against two,
+// and the rows are spread over half the workgroups that are resident (by two
+// launches where dx is written over dy or x).  bf16, one launch against two,
 // 1024 rows: 6.5 / 9.0 us at 1024 columns, 13.6 / 19.1 at 4096; 2048 rows:
 // 9.8 / 10.1 at 1024, 16.1 / 12.0 at 1536 columns.
 constexpr int64_t kDirectRows = 1024;
@@ -533,40 +534,58 @@ static void norm_bwd_t(const NormArgs& a, int grid, hipStream_t s) {
   });
 }
 
+// Whether dx shares memory with dy or x (it may be either).
+static bool norm_in_place(const NormCall& c) {
+  const int64_t size = c.dtype == GIFT_FP32 ? 4 : 2;
+  auto end = [&](const void* p, int64_t ld) { return (uintptr_t)p + (size_t)(((c.T - 1) * ld + c.d) * size); };
+  auto meet = [&](const void* p, int64_t ld) {
+    return p && c.T > 0 && (uintptr_t)p < end(c.y, c.ldy) && (uintptr_t)c.y < end(p, ld);
+  };
+  return meet(c.dy, c.lddy) || meet(c.x, c.ldx);
+}
+
 hipError_t launch_norm_backward(const NormCall& c, float* part, float* dw, float* db, int accumulate, hipStream_t s) {
   NormArgs a = norm_args(c);
   const int step = norm_step_rows(c.d);
   a.P = norm_partials(c.T, c.d);
   a.steplog = __builtin_ctz((unsigned)(norm_group_rows(c.d) / step));
   a.sums = db ? 2 : 1;
-  int grid = a.P;
-  if (c.T <= kDirectRows) {
+  const bool direct = c.T <= kDirectRows;
+  if (direct) {
     a.steplog = 0;
     const int64_t all = cdiv(c.T, step), most = c.d > 8192 ? 128 : c.d > 2048 ? 256 : 512;
     a.P = (int)(all < most ? all : most);
-    grid = a.P;
-    if (part) {
-      a.dw = dw;
-      a.db = db;
-      a.accumulate = accumulate;
-      grid += (int)cdiv(c.d, kActBlock);
-      part = nullptr;
-    }
+    a.dw = dw;
+    a.db = db;
+    a.accumulate = accumulate;
+  } else {
+    a.part = part;
   }
   a.groups = cdiv(c.T, step << a.steplog);
-  a.part = part;
-  if (c.ckpt) {
-    if (c.dtype == GIFT_BF16) norm_bwd_t<Bf16, true>(a, grid, s);
-    else if (c.dtype == GIFT_FP16) norm_bwd_t<Fp16, true>(a, grid, s);
-    else norm_bwd_t<float, true>(a, grid, s);
-  } else {
-    if (c.dtype == GIFT_BF16) norm_bwd_t<Bf16, false>(a, grid, s);
-    else if (c.dtype == GIFT_FP16) norm_bwd_t<Fp16, false>(a, grid, s);
-    else norm_bwd_t<float, false>(a, grid, s);
+  auto launch = [&](int grid) {
+    if (c.ckpt) {
+      if (c.dtype == GIFT_BF16) norm_bwd_t<Bf16, true>(a, grid, s);
+      else if (c.dtype == GIFT_FP16) norm_bwd_t<Fp16, true>(a, grid, s);
+      else norm_bwd_t<float, true>(a, grid, s);
+    } else {
+      if (c.dtype == GIFT_BF16) norm_bwd_t<Bf16, false>(a, grid, s);
+      else if (c.dtype == GIFT_FP16) norm_bwd_t<Fp16, false>(a, grid, s);
+      else norm_bwd_t<float, false>(a, grid, s);
+    }
+  };
+  const int rows = a.P, columns = direct && part ? (int)cdiv(c.d, kActBlock) : 0;
+  if (columns && norm_in_place(c)) {
+    // all columns are read before any row is written
+    a.P = 0;
+    launch(columns);
+    a.P = rows;
+    if (rows) launch(rows);
+  } else if (rows + columns) {
+    launch(rows + columns);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (part)
+  if (a.part)
     hipLaunchKernelGGL(k_norm_reduce, dim3((unsigned)cdiv(a.sums * (int64_t)c.d, kReduceCols)),
                        dim3(kReduceCols * kReduceRows), 0, s, part, a.P, c.d, a.sums * c.d, dw, db, accumulate);
   return hipGetLastError();

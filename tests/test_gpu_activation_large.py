@@ -153,6 +153,27 @@ def test_norm_backward_lane_groups(fw, T, d, dtype, kind):
         _check_backward(dx, dw, db, f64(dy), X, M, f64(rstd), f64(w), kind, DT[dtype])
 
 
+@pytest.mark.parametrize("T,d", [(1000, 4096), (1024, 520), (300, 12288)])
+def test_norm_backward_in_place_with_few_rows(fw, T, d):
+    """dx written over dy or over x: the parameter gradients still come from the
+    old values."""
+    x, dy = draw(T, d, torch.bfloat16, 1), draw(T, d, torch.bfloat16, 2)
+    w, b = _params(d, "bf16", "layer", "same", 3)
+    _, mean, rstd = fw.norm_forward(x, w, b)
+    dx, dw, db = fw.norm_backward(dy, x, mean, rstd, w)
+    M = f64(mean)
+    _check_backward(dx, dw, db, f64(dy), f64(x), M, f64(rstd), f64(w), "layer", torch.bfloat16)
+    for over_x in (False, True):
+        X, G = x.clone(), dy.clone()
+        dx2, dw2, db2 = fw.norm_backward(G, X, mean, rstd, w, dx=X if over_x else G)
+        _check_backward(dx2, dw2, db2, f64(dy), f64(x), M, f64(rstd), f64(w), "layer", torch.bfloat16)
+    ck = fw.ActCheckpoint(T, d, device=DEV).save(x)
+    G = dy.clone()
+    dx3, dw3, db3 = fw.norm_backward(G, ck, mean, rstd, w, dx=G)
+    _check_backward(dx3, dw3, db3, f64(dy), f64(ck.restore(torch.float32)), M, f64(rstd), f64(w), "layer",
+                    torch.bfloat16)
+
+
 def test_rms_bias_gradient_when_given(fw):
     T, d = 600, 1000
     x, dy = draw(T, d, torch.bfloat16, 8), draw(T, d, torch.bfloat16, 9)
