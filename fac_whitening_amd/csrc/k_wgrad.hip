@@ -61,7 +61,7 @@ __device__ __forceinline__ float elem_f32(const Fp16* p) { return (float)__built
 //  * Tokens past T read as zero on both sides (buffer bounds; exponents by a
 //    mask, they may hold anything).  A column chunk that crosses m is read
 //    shifted, ending at m - 1, and its outputs stored accordingly.
-// Measured at 1536 x 6144, 16384 tokens, bf16 delta: 296 us, 1.04 PFLOP/s (a
+// Measured at 1536 x 6144, 16384 tokens, bf16 delta: 286-296 us, 1.06 PFLOP/s (a
 // library product of the same shape on bf16 operands already converted: 380
 // us as token-major operands, 306 with tokens contiguous).  A stage of 64
 // tokens of a 256 x 256 tile takes about 2870 clocks: 2048 of them are the
@@ -553,46 +553,67 @@ __global__ void __launch_bounds__(256, MT * NT > 4 ? 1 : 2) k_wgrad(WgradArgs a)
 }
 
 // W of the split tiles from their pieces, added in token order.  Each
-// workgroup takes 1024 elements of one tile, four a thread.
+// workgroup takes 32 rows of one wave's part of a tile, 32 NT columns, and
+// turns them from the order of the registers (see the end of wgrad_segment)
+// to rows in LDS: W is written in row segments of 128 NT bytes (in the order
+// of the registers, 128 bytes a row at a time: 42 us instead of 28 at 1536 x
+// 6144, 101 MB of pieces).
 template <int MT, int NT>
 __global__ void __launch_bounds__(256) k_wgrad_join(WgradArgs a, int G, int first, int ca) {
-  constexpr int SA = 64 * MT, SB = 64 * NT, PER = MT * NT * 4;   // workgroups of a tile
+  constexpr int SA = 64 * MT, SB = 64 * NT, PER = MT * 4, COLS = 32 * NT;   // PER: workgroups of a tile
+  __shared__ float rows[32][COLS + 4];
   const int tile = first + blockIdx.x / PER, q = blockIdx.x % PER;
-  const int f = (q * 256 + threadIdx.x) * 4;
-  float4 s = {0.f, 0.f, 0.f, 0.f};
+  const int x = q % MT, wave = q / MT;
+  const int lane = threadIdx.x & 63, e = threadIdx.x >> 6;
+  const float* base = a.part + (wave * MT + x) * NT * 1024 + threadIdx.x * 4;
+  float4 s[NT];
+#pragma unroll
+  for (int y = 0; y < NT; ++y) s[y] = float4{0.f, 0.f, 0.f, 0.f};
   wgrad_pieces(wgrad_levels(a.nbm * a.nbn, (a.nst + a.unit - 1) / a.unit, G), tile, [&](int number, int stride, int count) {
-    for (int c = 0; c < count; c += 8) {   // eight loads in flight
-      float4 x[8];
+    constexpr int AT = 16 / NT;   // pieces at once: sixteen loads in flight
+    for (int c = 0; c < count; c += AT) {
+      float4 v[AT][NT];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[k] = float4{0.f, 0.f, 0.f, 0.f};
-        if (c + k < count)
-          x[k] = *reinterpret_cast<const float4*>(a.part + ((int64_t)number + (int64_t)(c + k) * stride) * SA * SB + f);
-      }
+      for (int k = 0; k < AT; ++k)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        s.x += x[k].x;
-        s.y += x[k].y;
-        s.z += x[k].z;
-        s.w += x[k].w;
-      }
+        for (int y = 0; y < NT; ++y) {
+          v[k][y] = float4{0.f, 0.f, 0.f, 0.f};
+          if (c + k < count)
+            v[k][y] = *reinterpret_cast<const float4*>(base + ((int64_t)number + (int64_t)(c + k) * stride) * SA * SB + y * 1024);
+        }
+#pragma unroll
+      for (int k = 0; k < AT; ++k)
+#pragma unroll
+        for (int y = 0; y < NT; ++y) {
+          s[y].x += v[k][y].x;
+          s[y].y += v[k][y].y;
+          s[y].z += v[k][y].z;
+          s[y].w += v[k][y].w;
+        }
     }
   });
+#pragma unroll
+  for (int y = 0; y < NT; ++y) {
+    const float v[4] = {s[y].x, s[y].y, s[y].z, s[y].w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) rows[8 * e + 4 * (lane >> 5) + r][32 * y + (lane & 31)] = v[r];
+  }
+  __syncthreads();
   int ti, tj;
   wgrad_tile(tile, a.nbm, a.nbn, ti, tj);
-  // this thread's four outputs (see the end of wgrad_segment)
-  const int lane = (f >> 2) & 63, e = (f >> 8) & 3, t = f >> 10;
-  const int y = t % NT, x = t / NT % MT, wave = t / (NT * MT);
-  const int j = tj * SB + 32 * ((wave & 1) * NT + y) + (lane & 31);
-  if (j >= a.d) return;
-  const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = wgrad_row(32 * ((wave >> 1) * MT + x) + 8 * e + 4 * (lane >> 5) + r, ca, a.m - ti * SA);
+  for (int k = 0; k < NT; ++k) {
+    const int f = k * 256 + threadIdx.x, r = f / (COLS / 4), c = f % (COLS / 4) * 4;
+    const int i = wgrad_row(32 * ((wave >> 1) * MT + x) + r, ca, a.m - ti * SA);
+    const int j = tj * SB + (wave & 1) * COLS + c;
     if (i < 0) continue;
     float* w = a.W + (int64_t)(ti * SA + i) * a.ldw + j;
-    const float o = a.alpha * v[r];
-    *w = a.accumulate ? *w + o : o;
+#pragma unroll
+    for (int l = 0; l < 4; ++l)
+      if (j + l < a.d) {
+        const float o = a.alpha * rows[r][c + l];
+        w[l] = a.accumulate ? w[l] + o : o;
+      }
   }
 }
 
@@ -731,7 +752,7 @@ template <typename TD, int FMT, int MT, int KT>
 void wgrad_go(const WgradArgs& a, const WgradPlan& p, hipStream_t s) {
   hipLaunchKernelGGL((k_wgrad<TD, FMT, MT, MT, KT>), dim3((unsigned)p.grid), dim3(256), 0, s, a);
   if (p.split)
-    hipLaunchKernelGGL((k_wgrad_join<MT, MT>), dim3((unsigned)(p.split * MT * MT * 4)), dim3(256), 0, s, a, p.grid,
+    hipLaunchKernelGGL((k_wgrad_join<MT, MT>), dim3((unsigned)(p.split * MT * 4)), dim3(256), 0, s, a, p.grid,
                        p.first, KT * MT / 32);
 }
 
