@@ -11,8 +11,9 @@
 // a value is exact in bf16.  The lower limit 32 keeps every value
 // at or above 2^-111, a normal bf16 and fp32 number: the conversions and the
 // matrix instructions never see a subnormal.  (2^-95 is far below any
-// activation; smaller blocks round to the subnormal codes and to zero.)  A block that holds an Inf or NaN is stored as e = 255 and
-// codes 0x7F, and its values are NaN.
+// activation; smaller blocks round to the subnormal codes and to zero.)  A
+// block that holds an Inf or NaN is stored as e = 255 and codes 0x7F, and its
+// values are NaN.
 //
 // Layout: codes [T][ldc], ldc a multiple of 32 with ldc >= d; the exponents
 // are [ceil(T / 8)][nb][8], nb = ceil(d / 32): the eight tokens that one

@@ -217,14 +217,7 @@ __global__ void __launch_bounds__(kNormThreads<G>) k_norm_fwd(NormArgs a) {
   }
 }
 
-// Backward.  Workgroup p takes the row groups p, p + P, ...; each lane keeps
-// the dgamma and dbeta sums of its own columns in registers over all of them
-// and has the next rows in flight while it works on the present one: two
-// (kAhead) where the registers of two resident workgroups allow it, one with
-// four chunks or three of fp32, none above 12288 columns (there the weights
-// come from the cache each time too).  The partial sums of the workgroups go
-// to part [P][sums][d] and are added in order by k_norm_reduce: no atomics,
-// the same result every time.
+// Rows in flight ahead of the present one (see k_norm_bwd).
 template <typename T, int G, int CH>
 constexpr int kAhead = G == 512 && CH == 4 ? 0 : CH <= 2 || (CH == 3 && sizeof(T) == 2) ? 2 : 1;
 
@@ -271,6 +264,15 @@ __device__ __forceinline__ void norm_columns(const NormArgs& a, int block, float
   }
 }
 
+// Backward.  Workgroup p takes the row groups p, p + P, ...; each lane keeps
+// the dgamma and dbeta sums of its own columns in registers over all of them
+// and has the next rows in flight while it works on the present one: two
+// (kAhead) where the registers of two resident workgroups allow it, one with
+// four chunks or three of fp32, none above 12288 columns (there the weights
+// come from the cache each time too).  The partial sums of the workgroups go
+// to part [P][sums][d] and are added in order by k_norm_reduce: no atomics,
+// the same result every time.  Up to kDirectRows rows the workgroups
+// past a.P sum the columns instead (norm_columns) and there is no part.
 template <typename T, bool CK, int G, int CH>
 __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
   constexpr int NT = kNormThreads<G>;
