@@ -6,7 +6,7 @@
 
 namespace {
 
-constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;   // workgroups of up to 512 threads: fewer than 2^32 threads
+using gift::kMaxGrid;
 constexpr int kMaxCols = 1 << 24;
 
 bool dtype_ok(int32_t t) { return t == GIFT_BF16 || t == GIFT_FP32 || t == GIFT_FP16; }
@@ -148,8 +148,8 @@ gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, in
   if (!rows_ok(d_delta, dtype, ldd, T, m) || !ckpt_ok(h_ckpt, T, d)) return GIFT_ERR_INVALID_ARG;
   if (!d_W || !aligned(d_W, 4) || ldw < d) return GIFT_ERR_INVALID_ARG;
   if (!d_work || !aligned(d_work, 16)) return GIFT_ERR_INVALID_ARG;
+  if (gift::wgrad_grid(m, d) > kMaxGrid) return GIFT_ERR_UNSUPPORTED;
   if (work_bytes < gift_weight_grad_workspace_bytes(T, m, d, dtype)) return GIFT_ERR_WORKSPACE;
-  if (gift::cdiv(m, 64) * gift::cdiv(d, 64) > kMaxGrid) return GIFT_ERR_UNSUPPORTED;
   gift::WgradCall c{};
   c.delta = d_delta;
   c.dtype = dtype;

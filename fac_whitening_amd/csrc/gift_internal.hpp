@@ -244,6 +244,7 @@ hipError_t launch_hits(const float* g, int64_t n, int fmt, const uint32_t* slot,
                        unsigned long long* counts, hipStream_t s);
 // Activation operators (k_act.hip, k_norm.hip, k_wgrad.hip).
 constexpr int kNormMaxCols = 16384;
+constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;   // workgroups of up to 512 threads: fewer than 2^32 threads
 // Keeps the HIP error for gift_last_hip_error; returns GIFT_ERR_HIP.
 gift_status hip_failure(hipError_t e);
 struct NormCall {
@@ -285,6 +286,9 @@ int norm_partials(int64_t T, int d);
 int64_t norm_forward_grid(int64_t T, int d);
 hipError_t launch_norm_forward(const NormCall& c, hipStream_t s);
 hipError_t launch_norm_backward(const NormCall& c, float* part, float* dw, float* db, int accumulate, hipStream_t s);
+// Workgroups of the weight gradient's vector-unit form, 64 x 64 outputs each
+// (the host refuses what exceeds a grid).
+int64_t wgrad_grid(int m, int d);
 size_t wgrad_workspace(int64_t T, int m, int d, int dtype);
 hipError_t launch_weight_grad(const WgradCall& c, hipStream_t s);
 

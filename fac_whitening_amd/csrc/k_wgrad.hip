@@ -686,6 +686,8 @@ __global__ void __launch_bounds__(256) k_wgrad_valu(WgradArgs a) {
 }
 
 
+int64_t wgrad_grid(int m, int d) { return cdiv(m, 64) * cdiv(d, 64); }
+
 namespace {
 
 struct WgradPlan {
@@ -734,6 +736,8 @@ WgradPlan wgrad_plan(int64_t T, int m, int d, int dtype, int64_t ldd, int64_t ld
   // offsets within a stage are 32 bits, and so are its counts of tiles and
   // stages; what is beyond runs on the vector units.
   if (m < 8 || T == 0 || ldd >= ((int64_t)1 << 31) / (64 * size) || ldc >= ((int64_t)1 << 31) / 64) return best;
+  // (an output beyond a launch's reach has no plan: its tiles alone can pass 32 bits)
+  if (wgrad_grid(m, d) > kMaxGrid) return best;
   if (T >= (int64_t)1 << 34 || cdiv(m, 128) * cdiv(d, 128) * cdiv(T, 64) >= (int64_t)1 << 38) return best;
   double least = 0;
   for (int variant = 1; variant <= 2; ++variant)
@@ -792,7 +796,7 @@ hipError_t launch_weight_grad(const WgradCall& c, hipStream_t s) {
   if (c.T == 0 && c.accumulate) return hipSuccess;
   const WgradPlan p = wgrad_plan(c.T, c.m, c.d, c.dtype, c.ldd, c.ckpt->ldc);
   if (p.variant == 0) {
-    const dim3 grid((unsigned)(cdiv(c.m, 64) * cdiv(c.d, 64)));
+    const dim3 grid((unsigned)wgrad_grid(c.m, c.d));
     if (c.dtype == GIFT_BF16) hipLaunchKernelGGL(k_wgrad_valu<Bf16>, grid, dim3(256), 0, s, a);
     else if (c.dtype == GIFT_FP16) hipLaunchKernelGGL(k_wgrad_valu<Fp16>, grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL(k_wgrad_valu<float>, grid, dim3(256), 0, s, a);
