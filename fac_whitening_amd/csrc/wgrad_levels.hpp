@@ -15,6 +15,7 @@ namespace gift {
 // and what is left of tiles, units, workgroups and C goes through the same
 // step again (the Euclidean algorithm on n and C).  Pieces of a level are
 // numbered from `base`; piece 0 .. R - 1 of a level is that of its tile.
+// Whole tiles have no pieces and take no numbers.
 struct WLevel {
   int R, n, W, C;      // tiles, units left of each, workgroups, units left for each
   int from;            // first unit of the pieces
@@ -36,7 +37,7 @@ struct WLevel {
       n -= q * C;
     } else {
       const int t = tiles();
-      base += t;
+      if (from > 0) base += t;   // (from == 0: whole tiles)
       C -= count() * n;
       R -= t;
       tile0 += t;
