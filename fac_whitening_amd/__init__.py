@@ -555,12 +555,13 @@ class Group:
 # What these functions allocate (outputs not given, workspaces) comes from the
 # allocator's pool of the stream they launch on, so it may be dropped as soon
 # as the call returns; tensors the caller passes are the caller's to order.
+# All operands of a call are on one device, the current one.
 
 # Small calls cost what the host does (a launch is about 4 us, a current_stream
 # object 3, an allocation 2), so these wrappers do each thing once.
 
-def _rows(t, what, T=None, n=None, dtype=None):
-    """Checks a [T][n] tensor with unit column stride; returns its leading dimension."""
+def _rows(t, what, T=None, n=None, dtype=None, device=None):
+    """Checks a [T][n] tensor with unit column stride (on `device`, or on any GPU); returns its leading dimension."""
     dt, shape = t.dtype, t.shape
     if dt not in DTYPES or len(shape) != 2 or (dtype is not None and dt != dtype):
         raise ValueError(f"{what} must be a [T][n] tensor of {dtype or 'bf16, fp16 or fp32'}")
@@ -570,8 +571,8 @@ def _rows(t, what, T=None, n=None, dtype=None):
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{what} must have unit column stride")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on the GPU")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{what} must be on {device or 'the GPU'}")
     return ld if rows > 1 else max(cols, 1)
 
 
@@ -598,11 +599,17 @@ def _empty_like(stream, t):
     return _empty(stream, t.shape, t.dtype, t.device)
 
 
-def _raw_stream(stream):
-    """Handle of the stream, or of the current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+def _raw_stream(stream, device):
+    """Handle of the stream, or of the current one, for a call whose operands are on `device`."""
+    here = torch._C._cuda_getDevice()
+    if device.index != here or (stream is not None and stream.device != device):
+        raise ValueError(f"operands on {device} need that device to be the current one, and its streams")
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
+
+
+def _on(device, t, what):
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}")
 
 
 _F32 = (torch.float32,)
@@ -643,18 +650,19 @@ class ActCheckpoint:
         return self.codes.numel() + self.bscales.numel()
 
     def save(self, x: torch.Tensor, stream=None):
-        ld = _rows(x, "x", self.T, self.d)
-        _check(_lib.gift_act_save(x.data_ptr(), DTYPES[x.dtype], ld, self.T, self.d, self._ref, _raw_stream(stream)),
-               "gift_act_save")
+        ld = _rows(x, "x", self.T, self.d, device=self.device)
+        _check(_lib.gift_act_save(x.data_ptr(), DTYPES[x.dtype], ld, self.T, self.d, self._ref,
+                                  _raw_stream(stream, self.device)), "gift_act_save")
         return self
 
     def restore(self, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+        raw = _raw_stream(stream, self.device)
         if out is None:
             out, ld = _empty(stream, (self.T, self.d), dtype, self.device), self.d
         else:
-            ld = _rows(out, "out", self.T, self.d)
-        _check(_lib.gift_act_restore(self._ref, self.T, self.d, out.data_ptr(), DTYPES[out.dtype], ld,
-                                     _raw_stream(stream)), "gift_act_restore")
+            ld = _rows(out, "out", self.T, self.d, device=self.device)
+        _check(_lib.gift_act_restore(self._ref, self.T, self.d, out.data_ptr(), DTYPES[out.dtype], ld, raw),
+               "gift_act_restore")
         return out
 
 
@@ -667,19 +675,22 @@ def norm_forward(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, kin
     kind = NORMS.get(kind, kind)
     ld = _rows(x, "x")
     (T, d), dev, dt = x.shape, x.device, x.dtype
+    raw = _raw_stream(stream, dev)
     wt = weight.dtype if weight is not None else bias.dtype if bias is not None else dt
     wp, bp = _vector(weight, "weight", d, _WEIGHTS[dt], dev), _vector(bias, "bias", d, (wt,), dev)
-    if ckpt is not None and (ckpt.T, ckpt.d) != (T, d):
-        raise ValueError("the checkpoint has another shape than x")
+    if ckpt is not None:
+        if (ckpt.T, ckpt.d) != (T, d):
+            raise ValueError("the checkpoint has another shape than x")
+        _on(dev, ckpt, "the checkpoint")
     if out is None:
         y, ldy = _empty_like(stream, x), d
     else:
-        y, ldy = out, _rows(out, "out", T, d, dt)
+        y, ldy = out, _rows(out, "out", T, d, dt, dev)
     mean = _empty(stream, (T,), torch.float32, dev) if kind == NORM_LAYER else None
     rstd = _empty(stream, (T,), torch.float32, dev)
     _check(_lib.gift_norm_forward(kind, x.data_ptr(), DTYPES[dt], ld, T, d, wp, bp, DTYPES[wt], eps, y.data_ptr(), ldy,
                                   None if mean is None else mean.data_ptr(), rstd.data_ptr(),
-                                  None if ckpt is None else ckpt._ref, _raw_stream(stream)), "gift_norm_forward")
+                                  None if ckpt is None else ckpt._ref, raw), "gift_norm_forward")
     return y, mean, rstd
 
 
@@ -691,13 +702,15 @@ def norm_backward(dy: torch.Tensor, x, mean, rstd, weight=None, kind="layer", dx
     kind = NORMS.get(kind, kind)
     ld = _rows(dy, "dy")
     (T, d), dev, dt = dy.shape, dy.device, dy.dtype
+    raw = _raw_stream(stream, dev)
     ck = x if isinstance(x, ActCheckpoint) else None
     if ck is not None:
         if (ck.T, ck.d) != (T, d):
             raise ValueError("the checkpoint has another shape than dy")
+        _on(dev, ck, "the checkpoint")
         ldx, xp = 0, None
     else:
-        ldx, xp = _rows(x, "x", T, d, dt), x.data_ptr()
+        ldx, xp = _rows(x, "x", T, d, dt, dev), x.data_ptr()
     wp = _vector(weight, "weight", d, _WEIGHTS[dt], dev)
     mp, rp = _vector(mean, "mean", T, _F32, dev), _vector(rstd, "rstd", T, _F32, dev)
     if accumulate and dweight is None and dbias is None:
@@ -719,13 +732,15 @@ def norm_backward(dy: torch.Tensor, x, mean, rstd, weight=None, kind="layer", dx
     if dx is None:
         dx, lddx = _empty_like(stream, dy), d
     else:
-        lddx = _rows(dx, "dx", T, d, dt)
+        lddx = _rows(dx, "dx", T, d, dt, dev)
     if work is None:
         work = _empty(stream, (_lib.gift_norm_workspace_bytes(T, d),), torch.uint8, dev)
+    else:
+        _on(dev, work, "work")
     _check(_lib.gift_norm_backward(kind, dy.data_ptr(), DTYPES[dt], ld, xp, ldx, None if ck is None else ck._ref,
                                    T, d, wp, DTYPES[dt if weight is None else weight.dtype], mp, rp, dx.data_ptr(),
-                                   lddx, dwp, dbp, int(accumulate), work.data_ptr(), work.numel(),
-                                   _raw_stream(stream)), "gift_norm_backward")
+                                   lddx, dwp, dbp, int(accumulate), work.data_ptr(), work.numel(), raw),
+           "gift_norm_backward")
     return dx, dweight, dbias
 
 
@@ -737,14 +752,18 @@ def weight_grad(delta: torch.Tensor, ckpt: ActCheckpoint, alpha: float = 1.0, ou
     T, d = ckpt.T, ckpt.d
     ld = _rows(delta, "delta", T)
     m, dev, dt = delta.shape[1], delta.device, DTYPES[delta.dtype]
+    raw = _raw_stream(stream, dev)
+    _on(dev, ckpt, "the checkpoint")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the tensor to add to")
         out, ldw = _empty(stream, (m, d), torch.float32, dev), d
     else:
-        ldw = _rows(out, "out", m, d, torch.float32)
+        ldw = _rows(out, "out", m, d, torch.float32, dev)
     if work is None:
         work = _empty(stream, (_lib.gift_weight_grad_workspace_bytes(T, m, d, dt),), torch.uint8, dev)
+    else:
+        _on(dev, work, "work")
     _check(_lib.gift_weight_grad(delta.data_ptr(), dt, ld, m, ckpt._ref, T, d, alpha, int(accumulate), out.data_ptr(),
-                                 ldw, work.data_ptr(), work.numel(), _raw_stream(stream)), "gift_weight_grad")
+                                 ldw, work.data_ptr(), work.numel(), raw), "gift_weight_grad")
     return out
