@@ -612,6 +612,14 @@ def _on(device, t, what):
         raise ValueError(f"{what} must be on {device}")
 
 
+def _bytes(device, t, what):
+    """Bytes behind the address of a dense tensor of any type."""
+    _on(device, t, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.numel() * t.element_size()
+
+
 _F32 = (torch.float32,)
 _WEIGHTS = {t: (t, torch.float32) for t in DTYPES}
 
@@ -735,11 +743,12 @@ def norm_backward(dy: torch.Tensor, x, mean, rstd, weight=None, kind="layer", dx
         lddx = _rows(dx, "dx", T, d, dt, dev)
     if work is None:
         work = _empty(stream, (_lib.gift_norm_workspace_bytes(T, d),), torch.uint8, dev)
+        wbytes = work.numel()
     else:
-        _on(dev, work, "work")
+        wbytes = _bytes(dev, work, "work")
     _check(_lib.gift_norm_backward(kind, dy.data_ptr(), DTYPES[dt], ld, xp, ldx, None if ck is None else ck._ref,
                                    T, d, wp, DTYPES[dt if weight is None else weight.dtype], mp, rp, dx.data_ptr(),
-                                   lddx, dwp, dbp, int(accumulate), work.data_ptr(), work.numel(), raw),
+                                   lddx, dwp, dbp, int(accumulate), work.data_ptr(), wbytes, raw),
            "gift_norm_backward")
     return dx, dweight, dbias
 
@@ -762,8 +771,9 @@ def weight_grad(delta: torch.Tensor, ckpt: ActCheckpoint, alpha: float = 1.0, ou
         ldw = _rows(out, "out", m, d, torch.float32, dev)
     if work is None:
         work = _empty(stream, (_lib.gift_weight_grad_workspace_bytes(T, m, d, dt),), torch.uint8, dev)
+        wbytes = work.numel()
     else:
-        _on(dev, work, "work")
+        wbytes = _bytes(dev, work, "work")
     _check(_lib.gift_weight_grad(delta.data_ptr(), dt, ld, m, ckpt._ref, T, d, alpha, int(accumulate), out.data_ptr(),
-                                 ldw, work.data_ptr(), work.numel(), raw), "gift_weight_grad")
+                                 ldw, work.data_ptr(), wbytes, raw), "gift_weight_grad")
     return out

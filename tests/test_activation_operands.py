@@ -123,3 +123,24 @@ def test_a_call_runs_on_its_operands_device(fw, name, monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
     call(**{k: f(D1) for k, f in makers.items()})
     assert len(fw._lib.calls) == 2 and fw._lib.calls[0][1][-1] == 7
+
+
+@pytest.mark.parametrize("name", ["norm_backward", "weight_grad"])
+def test_workspace_is_what_it_says_it_is(fw, name):
+    """The library writes as many bytes as it is told: they have to be there."""
+    call, makers = _calls(fw)[name]
+    need = 1 << 24
+
+    def with_work(work):
+        fw._lib.calls.clear()
+        call(**{**{k: f() for k, f in makers.items()}, "work": work})
+        ((_, args),) = fw._lib.calls
+        return args[-2]
+
+    assert with_work(Operand(need, dtype=torch.uint8)) == need
+    assert with_work(Operand(need // 4, dtype=F32)) == need
+    for bad in (Operand(need, dtype=torch.uint8, stride=(0,)), Operand(need, dtype=torch.uint8, stride=(2,)),
+                Operand(64, need // 64, dtype=torch.uint8, stride=(0, 1))):
+        with pytest.raises(ValueError):
+            with_work(bad)
+        assert not fw._lib.calls
