@@ -620,6 +620,13 @@ def _bytes(device, t, what):
     return t.numel() * t.element_size()
 
 
+def _kind(kind):
+    kind = NORMS.get(kind, kind)
+    if kind not in (NORM_LAYER, NORM_RMS):
+        raise ValueError(f"kind must be one of {', '.join(NORMS)}, not {kind!r}")
+    return kind
+
+
 _F32 = (torch.float32,)
 _WEIGHTS = {t: (t, torch.float32) for t in DTYPES}
 
@@ -666,6 +673,8 @@ class ActCheckpoint:
     def restore(self, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
         raw = _raw_stream(stream, self.device)
         if out is None:
+            if dtype not in DTYPES:
+                raise ValueError(f"a checkpoint restores to bf16, fp16 or fp32, not to {dtype}")
             out, ld = _empty(stream, (self.T, self.d), dtype, self.device), self.d
         else:
             ld = _rows(out, "out", self.T, self.d, device=self.device)
@@ -680,12 +689,13 @@ def norm_forward(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, kin
     returns y (of x's type), mean (None for "rms") and rstd, fp32 [T].  With
     `ckpt` (an ActCheckpoint of the same T and d) x is also saved there.
     weight and bias: of x's type or both fp32."""
-    kind = NORMS.get(kind, kind)
+    kind = _kind(kind)
     ld = _rows(x, "x")
     (T, d), dev, dt = x.shape, x.device, x.dtype
     raw = _raw_stream(stream, dev)
     wt = weight.dtype if weight is not None else bias.dtype if bias is not None else dt
-    wp, bp = _vector(weight, "weight", d, _WEIGHTS[dt], dev), _vector(bias, "bias", d, (wt,), dev)
+    wp = _vector(weight, "weight", d, _WEIGHTS[dt], dev)
+    bp = _vector(bias, "bias", d, _WEIGHTS[dt] if weight is None else (wt,), dev)
     if ckpt is not None:
         if (ckpt.T, ckpt.d) != (T, d):
             raise ValueError("the checkpoint has another shape than x")
@@ -707,7 +717,7 @@ def norm_backward(dy: torch.Tensor, x, mean, rstd, weight=None, kind="layer", dx
     """Backward of norm_forward.  x: the forward's input, or its ActCheckpoint.
     Returns dx (of dy's type), dweight and dbias (fp32 [d]; dbias None for
     "rms" unless given).  accumulate: added to the given dweight and dbias."""
-    kind = NORMS.get(kind, kind)
+    kind = _kind(kind)
     ld = _rows(dy, "dy")
     (T, d), dev, dt = dy.shape, dy.device, dy.dtype
     raw = _raw_stream(stream, dev)

@@ -144,3 +144,25 @@ def test_workspace_is_what_it_says_it_is(fw, name):
         with pytest.raises(ValueError):
             with_work(bad)
         assert not fw._lib.calls
+
+
+def test_wrong_types_and_kinds_are_value_errors(fw):
+    x, ck = Operand(T, DIM), _ckpt(fw)
+    v = lambda dt: Operand(DIM, dtype=dt)                    # noqa: E731
+    stats = Operand(T, dtype=F32)
+    calls = [
+        lambda: ck.restore(torch.float64), lambda: ck.restore(torch.uint8),
+        lambda: fw.norm_forward(x, None, v(torch.float64)), lambda: fw.norm_forward(x, None, v(torch.float16)),
+        lambda: fw.norm_forward(x, v(F32), v(BF16)), lambda: fw.norm_forward(x, v(torch.float16)),
+        lambda: fw.norm_forward(x, kind="batch"), lambda: fw.norm_forward(x, kind=None),
+        lambda: fw.norm_backward(x, x, stats, stats, kind="batch"),
+        lambda: fw.norm_backward(x, x, stats, stats, v(torch.float64)),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError):
+            call()
+            print("accepted", i)
+    assert not fw._lib.calls
+    fw.norm_forward(x, None, v(F32))
+    fw.norm_forward(x, None, v(BF16), kind=fw.NORM_LAYER)
+    assert [a[1][8] for a in fw._lib.calls] == [fw.FP32, fw.BF16]      # the bias alone gives the type
