@@ -637,7 +637,10 @@ class ActCheckpoint:
     [ceil(T / 8)][ceil(d / 32)][8] uint8, the biased exponent of the scale of
     each token and 32 columns.  Buffers that are not given are allocated (on
     `stream`'s pool); given ones are used as they are, so a checkpoint kept
-    elsewhere can be wrapped without a copy."""
+    elsewhere can be wrapped without a copy.  The buffers' addresses are taken
+    here: other buffers need another checkpoint."""
+
+    _FIXED = frozenset(("T", "d", "fmt", "codes", "bscales", "device"))
 
     def __init__(self, T: int, d: int, fmt=E4M3, codes=None, bscales=None, device="cuda", stream=None):
         self.T, self.d, self.fmt = int(T), int(d), FORMATS.get(fmt, fmt)
@@ -660,6 +663,11 @@ class ActCheckpoint:
         self._c = ActCkpt(codes.data_ptr(), codes.stride(0) if self.T > 1 else codes.shape[1] // 32 * 32,
                           bscales.data_ptr(), self.fmt)
         self._ref = ctypes.byref(self._c)
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and "_ref" in self.__dict__:
+            raise AttributeError(f"a checkpoint's {name} cannot be replaced")
+        super().__setattr__(name, value)
 
     def nbytes(self) -> int:
         return self.codes.numel() + self.bscales.numel()

@@ -166,3 +166,15 @@ def test_wrong_types_and_kinds_are_value_errors(fw):
     fw.norm_forward(x, None, v(F32))
     fw.norm_forward(x, None, v(BF16), kind=fw.NORM_LAYER)
     assert [a[1][8] for a in fw._lib.calls] == [fw.FP32, fw.BF16]      # the bias alone gives the type
+
+
+def test_a_checkpoint_keeps_the_buffers_it_was_made_with(fw):
+    """The library is given the addresses taken when it was made."""
+    ck = _ckpt(fw)
+    codes, bscales = ck.codes, ck.bscales
+    for name, v in (("codes", Operand(T, DIM, dtype=torch.uint8)), ("bscales", Operand(2, 2, 8, dtype=torch.uint8)),
+                    ("T", T + 1), ("d", DIM + 1), ("fmt", fw.E5M2), ("device", D1)):
+        with pytest.raises(AttributeError):
+            setattr(ck, name, v)
+    assert ck.codes is codes and ck.bscales is bscales and (ck.T, ck.d, ck.fmt) == (T, DIM, fw.E4M3)
+    ck.name = "fc1"                                          # a user's own attribute
