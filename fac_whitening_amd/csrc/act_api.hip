@@ -1,6 +1,7 @@
 // C entries of the activation operators: argument checks, then one or two
 // kernel launches on the caller's stream.  They keep no state.
 #include <cmath>
+#include <numeric>
 
 #include "gift_internal.hpp"
 
@@ -19,6 +20,20 @@ bool rows_ok(const void* p, int32_t dtype, int64_t ld, int64_t T, int32_t n) {
 }
 
 bool sizes_ok(int64_t T, int32_t d) { return T >= 0 && T < ((int64_t)1 << 40) && d >= 1 && d <= kMaxCols; }
+
+// Whether an output [T][n] at q may be written while rows of an input at p are
+// still to be read: it is the input itself, element for element, or shares no
+// byte with it.  Rows of both repeat every gcd of the strides, so rows side by
+// side in one buffer are told apart by their places within it.
+bool out_ok(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t T, int32_t n, int32_t dtype) {
+  if (T == 0 || !p) return true;
+  const __int128 size = dtype_size(dtype), a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  if (a == b && (ldp == ldq || T == 1)) return true;
+  if (a + ((T - 1) * (__int128)ldp + n) * size <= b || b + ((T - 1) * (__int128)ldq + n) * size <= a) return true;
+  if (T == 1) return false;
+  const __int128 g = std::gcd(ldp, ldq) * size, w = n * size, r = ((b - a) % g + g) % g;
+  return r >= w && g - r >= w;
+}
 
 bool ckpt_ok(const gift_act_ckpt* c, int64_t T, int32_t d) {
   if (!c || (c->fmt != GIFT_E4M3 && c->fmt != GIFT_E5M2)) return false;
@@ -62,6 +77,7 @@ gift_status gift_norm_forward(int32_t kind, const void* d_x, int32_t dtype, int6
     return GIFT_ERR_INVALID_ARG;
   if ((wdtype != dtype && wdtype != GIFT_FP32) || !(eps >= 0.0f) || !std::isfinite(eps)) return GIFT_ERR_INVALID_ARG;
   if (!rows_ok(d_x, dtype, ldx, T, d) || !rows_ok(d_y, dtype, ldy, T, d)) return GIFT_ERR_INVALID_ARG;
+  if (!out_ok(d_x, ldx, d_y, ldy, T, d, dtype)) return GIFT_ERR_INVALID_ARG;
   if (!aligned(d_gamma, dtype_size(wdtype)) || !aligned(d_beta, dtype_size(wdtype))) return GIFT_ERR_INVALID_ARG;
   if (!aligned(d_mean, 4) || !aligned(d_rstd, 4)) return GIFT_ERR_INVALID_ARG;
   if (h_ckpt && !ckpt_ok(h_ckpt, T, d)) return GIFT_ERR_INVALID_ARG;
@@ -104,6 +120,8 @@ gift_status gift_norm_backward(int32_t kind, const void* d_dy, int32_t dtype, in
   } else if (!rows_ok(d_x, dtype, ldx, T, d)) {
     return GIFT_ERR_INVALID_ARG;
   }
+  if (!out_ok(d_dy, lddy, d_dx, lddx, T, d, dtype) || !out_ok(d_x, ldx, d_dx, lddx, T, d, dtype))
+    return GIFT_ERR_INVALID_ARG;
   if (T > 0 && (!d_rstd || (kind == GIFT_NORM_LAYER && !d_mean))) return GIFT_ERR_INVALID_ARG;
   if (!aligned(d_mean, 4) || !aligned(d_rstd, 4) || !aligned(d_dgamma, 4) || !aligned(d_dbeta, 4) ||
       !aligned(d_gamma, dtype_size(wdtype)))

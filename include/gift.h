@@ -457,7 +457,8 @@ gift_status gift_act_restore(const gift_act_ckpt* h_ckpt, int64_t T, int32_t d, 
  * beta [d] are of type wdtype (`dtype` or GIFT_FP32); NULL: ones, zeros. */
 enum gift_norm { GIFT_NORM_LAYER = 0, GIFT_NORM_RMS = 1 };
 /* d_mean, d_rstd: fp32 [T] outputs for the backward pass, either may be NULL.
- * h_ckpt: also save x there (NULL: do not).  d_y may be d_x. */
+ * h_ckpt: also save x there (NULL: do not).  d_y may be d_x, with the same
+ * leading dimension; a d_y that shares memory with d_x in any other way is refused. */
 gift_status gift_norm_forward(int32_t kind, const void* d_x, int32_t dtype, int64_t ldx, int64_t T, int32_t d,
                               const void* d_gamma, const void* d_beta, int32_t wdtype, float eps, void* d_y,
                               int64_t ldy, float* d_mean, float* d_rstd, const gift_act_ckpt* h_ckpt,
@@ -470,7 +471,7 @@ size_t gift_norm_workspace_bytes(int64_t T, int32_t d);
  *                                               what they hold, for micro-batches)
  * x comes from d_x or, when that is NULL, from the checkpoint h_ckpt (one
  * of the two is given, not both).  d_mean (layer norm only) and d_rstd are the forward's.  d_dx may be
- * d_dy or d_x.  d_work: 16-byte aligned (NULL when no parameter gradient is asked for). */
+ * d_dy or d_x, with the same leading dimension; any other overlap with them is refused.  d_work: 16-byte aligned (NULL when no parameter gradient is asked for). */
 gift_status gift_norm_backward(int32_t kind, const void* d_dy, int32_t dtype, int64_t lddy, const void* d_x,
                                int64_t ldx, const gift_act_ckpt* h_ckpt, int64_t T, int32_t d, const void* d_gamma,
                                int32_t wdtype, const float* d_mean, const float* d_rstd, void* d_dx, int64_t lddx,
