@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_activation import DEV, DT, _params, draw
+from tests.test_gpu_activation import DEV, DT, U, _params, draw, strided
+from tests.test_gpu_activation_large import _wgrad64
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +35,95 @@ def test_norm_rows_side_by_side(fw, T, d):
     assert torch.equal(vx, x) and torch.equal(vdy, dy) and (buf[:, 4 * d:] == 0).all()
     with pytest.raises(fw.GiftError):
         fw.norm_forward(vx, w, b, out=buf[:, 8:8 + d])
+
+
+# -- weight gradients of 256 x 256 tiles whose tokens are split over workgroups ----
+# Pieces of 128 x 128 tiles need less than 64 MiB whatever the sizes (at most
+# 1020 of them, 64 KiB each), so a larger workspace says which form runs.
+
+def _large_split(fw, T, m, d, dtype):
+    need = fw._lib.gift_weight_grad_workspace_bytes(T, m, d, fw.DTYPES[DT[dtype]])
+    assert need > 64 << 20, "this size is to be computed in pieces of 256 x 256 tiles: take another"
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,m,d,ld,off", [(8192, 1024, 4096, None, 0), (8201, 1021, 4090, 1023, 1),
+                                          (1000, 1533, 6130, 1535, 1)])     # (bf16: whole tiles, cut at both edges)
+def test_weight_grad_large_tiles(fw, T, m, d, ld, off, dtype, fmt):
+    """Against 64 bits; fp32 chains of at most T / 4 + 64 additions."""
+    print(f"[wgrad T {T} {m}x{d} ld {ld} off {off} {dtype} {fmt}]", flush=True)
+    if T > 8000:
+        _large_split(fw, T, m, d, dtype)
+    ck = fw.ActCheckpoint(T, d, fmt, device=DEV).save(draw(T, d, torch.bfloat16, T + d))
+    if T % 8:
+        ck.bscales[-1, :, T % 8:] = 255
+    delta = draw(T, m, DT[dtype], T + m, 0.01, ld, off)
+    W = strided(m, d, torch.float32, d + 5, 3)
+    fw.weight_grad(delta, ck, alpha=1.0 / T, out=W)
+    ref, mag = _wgrad64(delta, ck, 1.0)
+    alpha = float(np.float32(1.0 / T))
+    assert ((W.double() - alpha * ref).abs() <= (T / 4 + 64) * U * alpha * mag + 1e-37).all()
+    mask = torch.ones_like(W._base, dtype=torch.bool)
+    torch.as_strided(mask, W.shape, W.stride(), W.storage_offset()).fill_(False)
+    assert (W._base[mask] == 777.0).all()
+    old = W.double()
+    fw.weight_grad(delta, ck, alpha=0.25, out=W, accumulate=True)
+    assert ((W.double() - 0.25 * ref - old).abs() <= (T / 4 + 64) * U * (0.25 * mag + old.abs()) + 1e-37).all()
+    assert (W._base[mask] == 777.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_weight_grad_nonfinite_in_large_split_tiles(fw, dtype, fmt):
+    T, m, d = 8192, 1024, 4096
+    _large_split(fw, T, m, d, dtype)
+    x = draw(T, d, torch.float32, 3)
+    x[8190, 3000] = float("nan")
+    ck = fw.ActCheckpoint(T, d, fmt, device=DEV).save(x)
+    delta = draw(T, m, DT[dtype], 4)
+    delta[3, 700], delta[8191, 1000] = -float("inf"), float("nan")
+    W = fw.weight_grad(delta, ck)
+    bad = torch.zeros(m, d, dtype=torch.bool, device=DEV)
+    bad[:, 3000 // 32 * 32:3000 // 32 * 32 + 32] = True
+    bad[700] = bad[1000] = True
+    assert torch.equal(~torch.isfinite(W), bad)
+    # an infinity times a finite value keeps its sign
+    a = ck.restore(torch.float32)[3]
+    ok = torch.isfinite(a) & (a != 0) & ~bad[0]
+    assert ok.sum() > d - 40 - (a == 0).sum() and (W[700][ok] == -torch.sign(a[ok]) * float("inf")).all()
+
+
+def _one_token_a_column(fw, T, m, d, dtype, fmt, scale, seed):
+    """delta and checkpoint for which each output is one product: column j of
+    the activation is not zero at one token alone, where it is a power of two,
+    and delta has all the bits its type holds (odd integers times scale)."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    bits = {"bf16": 8, "fp16": 11, "fp32": 24}[dtype]
+    toks = torch.randperm(T, generator=g, device=DEV)[:59]
+    toks[0], toks[1] = 0, T - 1
+    tok = toks[torch.arange(d, device=DEV) % toks.numel()]
+    x = torch.zeros(T, d, device=DEV)
+    pw = torch.randint(-3, 4, (d,), generator=g, device=DEV)
+    x[tok, torch.arange(d, device=DEV)] = torch.exp2(pw.double()).float()
+    ck = fw.ActCheckpoint(T, d, fmt, device=DEV).save(x)
+    assert torch.equal(ck.restore(torch.float32), x)
+    n = torch.randint(1 << (bits - 2), 1 << (bits - 1), (T, m), generator=g, device=DEV) * 2 + 1
+    n = torch.where(torch.rand(T, m, generator=g, device=DEV) < 0.5, -n, n)
+    delta = (n.double() * scale).to(DT[dtype])
+    assert torch.equal(delta.double(), n.double() * scale)
+    return delta, ck, delta.double()[tok].t() * x.double()[tok, torch.arange(d, device=DEV)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,m,d", [(8201, 1021, 4090), (2048, 512, 2048), (700, 1530, 2100)])
+def test_weight_grad_keeps_all_bits_in_every_form(fw, T, m, d, dtype, fmt):
+    """Every sum is exact whatever the order, so W is, to the last of delta's bits."""
+    if T > 8000:
+        _large_split(fw, T, m, d, dtype)
+    delta, ck, want = _one_token_a_column(fw, T, m, d, dtype, fmt, 1.0, T + m)
+    W = fw.weight_grad(delta, ck)
+    assert torch.equal(W.double(), want)
+    fw.weight_grad(delta, ck, out=W, accumulate=True, alpha=-1.0)
+    assert (W == 0).all()
