@@ -42,7 +42,9 @@ __device__ __forceinline__ float elem_f32(const Fp16* p) { return (float)__built
 //    bf16; delta enters as P bf16 planes whose sum is delta: bf16 itself, fp16
 //    (11 bits) as two, fp32 (24 bits) as three, each the leading 8 bits of
 //    what the planes before it leave (truncation: no plane overflows, the
-//    remainders are exact).  Products are exact in fp32, sums are fp32.
+//    remainders are exact).  A plane's last bit is 2^-133 at least: an fp32
+//    value below 2^-110 loses its bits under that.  Products are exact in
+//    fp32, sums are fp32.
 //  * The operands want 8 consecutive tokens of a column per lane; memory has
 //    tokens in rows.  A thread loads 8 tokens x CA (CB) columns into registers,
 //    converts the codes (v_cvt_scalef32_pk_bf16: two columns of one token

@@ -480,7 +480,8 @@ gift_status gift_norm_backward(int32_t kind, const void* d_dy, int32_t dtype, in
 
 /* W [m][ldw] = alpha delta^T a (+ W when accumulate != 0), delta [T][ldd] of
  * type `dtype`, a [T][d] the values of the checkpoint.  delta enters the products
- * without loss (an fp32 value as the sum of three bf16 numbers, an fp16 value of two), a is
+ * without loss (an fp32 value as the sum of three bf16 numbers, an fp16 value of two; of
+ * fp32 values below 2^-110 what lies under 2^-133, the smallest bf16 number, is dropped), a is
  * exact in bf16, sums are fp32, added in the same order on every call.  d_work:
  * gift_weight_grad_workspace_bytes, 16-byte aligned, free to be used again by
  * what follows on the stream (partial sums of output tiles whose tokens are

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_activation import DEV, DT, U, _params, draw, strided
+from oracle import activation as A
+from tests.test_gpu_activation import DEV, DT, U, _params, draw, f64, strided
 from tests.test_gpu_activation_large import _wgrad64
 
 pytestmark = pytest.mark.gpu
@@ -127,3 +128,19 @@ def test_weight_grad_keeps_all_bits_in_every_form(fw, T, m, d, dtype, fmt):
     assert torch.equal(W.double(), want)
     fw.weight_grad(delta, ck, out=W, accumulate=True, alpha=-1.0)
     assert (W == 0).all()
+
+
+@pytest.mark.parametrize("T,m,d", [(8201, 1021, 4090), (2048, 512, 2048), (64, 4, 64)])
+def test_weight_grad_of_tiny_gradients(fw, T, m, d):
+    """fp32 gradients whose last bit is 2^-133, the smallest bf16 number, lose
+    nothing.  Of smaller ones the matrix-core form (m >= 8) drops what lies
+    below that bit: less than 2^-133 for each, times the activation."""
+    delta, ck, want = _one_token_a_column(fw, T, m, d, "fp32", "e4m3", 2.0 ** -133, 5)
+    assert torch.equal(fw.weight_grad(delta, ck).double(), want)
+    ck = fw.ActCheckpoint(T, d, device=DEV).save(draw(T, d, torch.float32, 6, 2.0 ** 40))
+    sums = ck.restore(torch.float32).double().abs().sum(0)
+    for e in (-118, -126, -133, -140):
+        delta = (draw(T, m, torch.float32, 7).double() * 2.0 ** e).float()
+        ref, mag = _wgrad64(delta, ck, 1.0)
+        lost = 2.0 ** -133 * sums if m >= 8 else 0 * sums
+        assert ((fw.weight_grad(delta, ck).double() - ref).abs() <= (T / 4 + 64) * U * mag + lost).all(), e
