@@ -6,9 +6,12 @@
 // kept as a biased exponent e (the fp32 exponent field): the smallest e >= 32
 // with amax <= FMAX 2^(e - 127), so no code saturates.  code = RNE(x 2^(127 -
 // e)), value = code 2^(e - 127).  A power of two makes both multiplications
-// exact: the only rounding of the round trip is the one to the 4 (E4M3) or 3
-// (E5M2) significant bits of a code, at most 2^-4 or 2^-3 of the value, and
-// a value is exact in bf16.  The lower limit 32 keeps every value
+// exact: the only rounding of the round trip is the one to a code.  It is off
+// by at most 2^-4 (E4M3: 4 significant bits) or 2^-3 (E5M2: 3) of the value,
+// or, for elements so far below their block's largest that they get a
+// subnormal code, by half the step of those: 2^-10 2^(e - 127) or 2^-17 2^(e -
+// 127).  A value is exact in bf16, but for 2^128, to which elements in the
+// last half step of fp32's range round.  The lower limit 32 keeps every value
 // at or above 2^-111, a normal bf16 and fp32 number: the conversions and the
 // matrix instructions never see a subnormal.  (2^-95 is far below any
 // activation; smaller blocks round to the subnormal codes and to zero.)  A

@@ -446,7 +446,9 @@ size_t gift_act_scale_bytes(int64_t T, int32_t d);   /* 0 for invalid sizes */
 /* d_x [T][ldx] -> checkpoint. */
 gift_status gift_act_save(const void* d_x, int32_t dtype, int64_t ldx, int64_t T, int32_t d,
                           const gift_act_ckpt* h_ckpt, gift_stream_t stream);
-/* checkpoint -> d_out [T][ldo] (bf16 and fp32 hold every value exactly; fp16 rounds to nearest even). */
+/* checkpoint -> d_out [T][ldo].  bf16 and fp32 hold every value exactly but 2^128, which is Inf there: elements
+ * from 1.9375 2^127 on (GIFT_E5M2: 1.875 2^127) round to it.  fp16 rounds to nearest even, values past its range to
+ * Inf: fp16 elements from 63488 on (GIFT_E5M2: 61440) have the value 65536. */
 gift_status gift_act_restore(const gift_act_ckpt* h_ckpt, int64_t T, int32_t d, void* d_out, int32_t dtype,
                              int64_t ldo, gift_stream_t stream);
 

@@ -144,3 +144,27 @@ def test_weight_grad_of_tiny_gradients(fw, T, m, d):
         ref, mag = _wgrad64(delta, ck, 1.0)
         lost = 2.0 ** -133 * sums if m >= 8 else 0 * sums
         assert ((fw.weight_grad(delta, ck).double() - ref).abs() <= (T / 4 + 64) * U * mag + lost).all(), e
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_checkpoint_of_the_largest_numbers(fw, fmt):
+    """Nothing saturates: what rounds to the next power of two past a type's
+    range restores to an infinity there, as any rounding to fewer bits does."""
+    top = torch.finfo(torch.float32).max
+    edge = (1.9375 if fmt == "e4m3" else 1.875) * 2.0 ** 127      # half way from the last code to 2^128
+    x = torch.full((4, 64), 1.0, device=DEV)
+    x[0, 0], x[1, 0], x[2, 0], x[3, 0] = top, edge, np.nextafter(np.float32(edge), np.float32(0)).item(), -top
+    ck = fw.ActCheckpoint(4, 64, fmt, device=DEV).save(x)
+    codes, e = A.ckpt_save(f64(x), fmt)
+    want = A.ckpt_values(codes, e, 64, fmt)
+    assert np.array_equal(ck.codes.cpu().numpy(), codes) and abs(want[[0, 1, 3], 0]).min() == 2.0 ** 128
+    with np.errstate(over="ignore"):
+        w32 = want.astype(np.float32).astype(np.float64)
+    for t in (torch.float32, torch.bfloat16):
+        assert np.array_equal(f64(ck.restore(t)), w32)
+    assert np.isfinite(w32[2]).all() and np.isposinf(w32[:2, 0]).all() and np.isneginf(w32[3, 0])
+    h = torch.full((4, 32), 65504.0, dtype=torch.float16, device=DEV)
+    h[1], h[2], h[3] = 63488.0, 61440.0, 61408.0
+    ck = fw.ActCheckpoint(4, 32, fmt, device=DEV).save(h)
+    assert torch.isinf(ck.restore(torch.float16)[:, 0]).tolist() == [True, True, fmt == "e5m2", False]
+    assert ck.restore(torch.float32)[0, 0].item() == 65536.0 and ck.restore()[0, 0].item() == 65536.0
