@@ -571,7 +571,7 @@ def _rows(t, what, T=None, n=None, dtype=None, device=None):
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{what} must have unit column stride")
-    if not t.is_cuda or (device is not None and t.device != device):
+    if not t.is_cuda if device is None else t.device != device:
         raise ValueError(f"{what} must be on {device or 'the GPU'}")
     return ld if rows > 1 else max(cols, 1)
 
@@ -643,15 +643,15 @@ class ActCheckpoint:
     _FIXED = frozenset(("T", "d", "fmt", "codes", "bscales", "device"))
 
     def __init__(self, T: int, d: int, fmt=E4M3, codes=None, bscales=None, device="cuda", stream=None):
-        self.T, self.d, self.fmt = int(T), int(d), FORMATS.get(fmt, fmt)
-        if self.T < 0 or self.d < 1 or self.fmt not in (E4M3, E5M2):
+        T, d, fmt = int(T), int(d), FORMATS.get(fmt, fmt)
+        if T < 0 or d < 1 or fmt not in (E4M3, E5M2):
             raise ValueError("a checkpoint needs T >= 0, d >= 1 and the format E4M3 or E5M2")
-        nb, groups = -(-self.d // 32), -(-self.T // 8)
+        nb, groups = -(-d // 32), -(-T // 8)
         if codes is None:
-            codes = _empty(stream, (self.T, nb * 32), torch.uint8, device)
-        elif codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[0] != self.T or (
+            codes = _empty(stream, (T, nb * 32), torch.uint8, device)
+        elif codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[0] != T or (
                 codes.shape[1] < nb * 32) or codes.stride(1) != 1:
-            raise ValueError(f"codes must be a uint8 [{self.T}][>= {nb * 32}] tensor on the GPU with unit column stride")
+            raise ValueError(f"codes must be a uint8 [{T}][>= {nb * 32}] tensor on the GPU with unit column stride")
         if not codes.is_cuda:
             raise ValueError("a checkpoint must be on the GPU")
         if bscales is None:
@@ -659,13 +659,12 @@ class ActCheckpoint:
         elif bscales.dtype != torch.uint8 or bscales.numel() != groups * nb * 8 or not bscales.is_contiguous() or (
                 bscales.device != codes.device):
             raise ValueError(f"bscales must be a contiguous uint8 [{groups}][{nb}][8] tensor beside the codes")
-        self.codes, self.bscales, self.device = codes, bscales, codes.device
-        self._c = ActCkpt(codes.data_ptr(), codes.stride(0) if self.T > 1 else codes.shape[1] // 32 * 32,
-                          bscales.data_ptr(), self.fmt)
-        self._ref = ctypes.byref(self._c)
+        c = ActCkpt(codes.data_ptr(), codes.stride(0) if T > 1 else codes.shape[1] // 32 * 32, bscales.data_ptr(), fmt)
+        self.__dict__.update(T=T, d=d, fmt=fmt, codes=codes, bscales=bscales, device=codes.device, _c=c,
+                             _ref=ctypes.byref(c))
 
     def __setattr__(self, name, value):
-        if name in self._FIXED and "_ref" in self.__dict__:
+        if name in self._FIXED:
             raise AttributeError(f"a checkpoint's {name} cannot be replaced")
         super().__setattr__(name, value)
 
