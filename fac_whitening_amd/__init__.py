@@ -555,7 +555,9 @@ class Group:
 # What these functions allocate (outputs not given, workspaces) comes from the
 # allocator's pool of the stream they launch on, so it may be dropped as soon
 # as the call returns; tensors the caller passes are the caller's to order.
-# All operands of a call are on one device, the current one.
+# All operands of a call are on one device, the current one.  The functions
+# record no graph, also where an operand requires a gradient: a module of
+# theirs calls the backward functions from its own torch.autograd.Function.
 
 # Small calls cost what the host does (a launch is about 4 us, a current_stream
 # object 3, an allocation 2), so these wrappers do each thing once.

@@ -168,7 +168,7 @@ __device__ __forceinline__ void pack8(const float* v, Raw8<float>& r) {
 // An output larger than the L2 caches of the eight dies together (4 MB each)
 // is gone from them before anyone reads it: written past them it leaves them
 // to the inputs (norm forward, 16384 x 1536 bf16: 28.1 -> 20.6 us; save and
-// restore, 16384 x 6144 bf16: 129 -> 106 us).  Smaller outputs stay cached
+// restore, 16384 x 6144 bf16: 120 -> 98 us).  Smaller outputs stay cached
 // for the next kernel.
 constexpr int64_t kStreamBytes = (int64_t)32 << 20;
 

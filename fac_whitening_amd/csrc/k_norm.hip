@@ -266,13 +266,19 @@ __device__ __forceinline__ void norm_columns(const NormArgs& a, int block, float
 
 // Backward.  Workgroup p takes the row groups p, p + P, ...; each lane keeps
 // the dgamma and dbeta sums of its own columns in registers over all of them
-// and has the next rows in flight while it works on the present one: two
-// (kAhead) where the registers of two resident workgroups allow it, one with
-// four chunks or three of fp32, none above 12288 columns (there the weights
-// come from the cache each time too).  The partial sums of the workgroups go
-// to part [P][sums][d] and are added in order by k_norm_reduce: no atomics,
-// the same result every time.  Up to kDirectRows rows the workgroups
-// past a.P sum the columns instead (norm_columns) and there is no part.
+// and has the next rows in flight while it works on the present one
+// (kAhead): two up to two chunks, or three of a 16-bit type, one with four
+// chunks or three of fp32, none above 12288 columns (there the weights come
+// from the cache each time too).  Two waves a SIMD are resident: up to two
+// chunks (90 to 192 registers) by the number of workgroups launched
+// (norm_partials), with three (211 to 232) and, from a 16-bit input, with
+// four (at most 255) by the registers.  Four chunks from a checkpoint or from
+// fp32 take 257 to 289 up to 8192 columns, and one wave is (8192 x 2048 bf16:
+// 34.7 us from a checkpoint, 26.6 from the input, which has more to read).
+// The partial sums of the workgroups go to part [P][sums][d] and are added in
+// order by k_norm_reduce: no atomics, the same result every time.  Up to
+// kDirectRows rows the workgroups past a.P sum the columns instead
+// (norm_columns) and there is no part.
 template <typename T, bool CK, int G, int CH>
 __global__ void __launch_bounds__(kNormThreads<G>) k_norm_bwd(NormArgs a) {
   constexpr int NT = kNormThreads<G>;
@@ -461,9 +467,11 @@ static int norm_group_rows(int d) { return d <= 128 ? 16 : 8; }
 // Rows of a step of a workgroup.
 static int norm_step_rows(int d) { return d <= 128 ? 16 : d <= 2048 ? 4 : 1; }
 
-// Workgroups of the backward pass: as many as are resident (two of 256
-// threads a compute unit, one of 512; every further one adds 8 d bytes of
-// partial sums to write and read), never more than there are row groups.
+// Workgroups of the backward pass: two of 256 threads a compute unit or one of
+// 512 (every further one adds 8 d bytes of partial sums to write and read),
+// never more than there are row groups.  They are resident together but for
+// the four-chunk variants of more than 256 registers (k_norm_bwd), which take
+// two rounds.
 int norm_partials(int64_t T, int d) {
   const int64_t g = cdiv(T, norm_group_rows(d)), most = d > 8192 ? 256 : 512;
   return (int)(g < most ? (g > 0 ? g : 1) : most);
@@ -471,8 +479,9 @@ int norm_partials(int64_t T, int d) {
 
 // Up to this many rows the parameter gradients are made in the same launch,
 // by workgroups of their own that read x and dy once more (from the cache),
-// and the rows are spread over half the workgroups that are resident (by two
-// launches where dx is written over dy or x).  bf16, one launch against two,
+// and the rows are spread over as many workgroups as above up to 2048 columns,
+// over half as many beyond (by two launches where dx is written over dy or x).
+// The workspace is not used then.  bf16, one launch against two,
 // 1024 rows: 6.5 / 9.0 us at 1024 columns, 13.6 / 19.1 at 4096; 2048 rows:
 // 9.8 / 10.1 at 1024, 16.1 / 12.0 at 1536 columns.
 constexpr int64_t kDirectRows = 1024;

@@ -533,7 +533,9 @@ __device__ __forceinline__ void wgrad_segment(const WgradArgs& a, char* lds, int
 // One workgroup's pieces (WLevel).  Workgroups of one die have consecutive
 // numbers.  A piece that is not a whole tile goes to part at its number, and
 // k_wgrad_join adds the pieces of a tile in token order: no atomics, the same
-// sums every time.
+// sums every time.  (128 x 128 tiles: two workgroups fit a compute unit with
+// bf16 delta, 64 KB of LDS each; with fp16 and fp32 the planes take 96 and 128
+// KB and one fits, whatever the bound below allows in registers.)
 template <typename TD, int FMT, int MT, int NT, int KT>
 __global__ void __launch_bounds__(256, MT * NT > 4 ? 1 : 2) k_wgrad(WgradArgs a) {
   using C = WTile<TD, FMT, MT, NT, KT>;
@@ -705,7 +707,8 @@ struct WgradPlan {
 // written and read.  Per 64 tokens a workgroup takes (measured; bf16, fp16,
 // fp32 delta):
 //   256 x 256  1.6, 3.8, 5.4      one workgroup a compute unit
-//   128 x 128  1.3, 1.3, 1.8      bf16: two workgroups a compute unit, 0.9 where there are no more than units
+//   128 x 128  1.3, 1.3, 1.8      bf16: two workgroups a compute unit, 0.9 where there are no more than units;
+//                                 fp16, fp32: one (see k_wgrad)
 // and 14 or 2.5 for each whole tile that it writes (128 tokens, 1536 x 6144: 33
 // against 22 us with the larger and the smaller tiles).
 double wgrad_try(WgradPlan& p, int variant, int units, int64_t T, int m, int d, int dtype) {
