@@ -63,7 +63,7 @@ __device__ __forceinline__ float elem_f32(const Fp16* p) { return (float)__built
 //  * Tokens past T read as zero on both sides (buffer bounds; exponents by a
 //    mask, they may hold anything).  A column chunk that crosses m is read
 //    shifted, ending at m - 1, and its outputs stored accordingly.
-// Measured at 1536 x 6144, 16384 tokens, bf16 delta: 286-296 us, 1.06 PFLOP/s (a
+// Measured at 1536 x 6144, 16384 tokens, bf16 delta: 283-298 us, 1.06 PFLOP/s (a
 // library product of the same shape on bf16 operands already converted: 380
 // us as token-major operands, 306 with tokens contiguous).  A stage of 64
 // tokens of a 256 x 256 tile takes about 2870 clocks: 2048 of them are the
