@@ -419,6 +419,7 @@ gift_status gift_group_decode_reduce(gift_group_t group, gift_stream_t stream);
  * of elements may start anywhere: pointers need the alignment of their
  * element type only, and a leading dimension is any number >= the row length
  * (16-byte aligned rows are the fastest).  T = 0 is valid everywhere.
+ * Sizes whose workgroups no single launch holds (2^23 and more) are GIFT_ERR_UNSUPPORTED.
  * Non-finite elements give what IEEE arithmetic gives; there is no flag.
  * All results are the same on every call (no atomics) and every call may be
  * captured into a graph.
