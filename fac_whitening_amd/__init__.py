@@ -30,12 +30,14 @@ E4M3, E5M2, E2M1 = 0, 1, 2
 SCALE_TENSOR, SCALE_BLOCK128, SCALE_BLOCK16, SCALE_BLOCK512 = 0, 1, 2, 3
 BF16, FP32, FP16 = 0, 1, 2   # FP16: activation operators only
 NORM_LAYER, NORM_RMS = 0, 1
+ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SIGMOID = range(5)
 SIDE_A, SIDE_G = 0, 1
 LAYER_TRANSIENT_STATS = 1   # statistics windows committed in one call, S in the workspace
 FLAG_NONFINITE, FLAG_SPIN_TIMEOUT = 1, 2
 TRANSFORMS = {"euclid": EUCLID, "diag": DIAG, "lowrank": LOWRANK, "chol": CHOL_INPUT, "twosided": CHOL_TWOSIDED}
 FORMATS = {"e4m3": E4M3, "e5m2": E5M2}
 NORMS = {"layer": NORM_LAYER, "rms": NORM_RMS}
+ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU, "sigmoid": ACT_SIGMOID}
 DTYPES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float16: FP16}
 SCALINGS = {"tensor": SCALE_TENSOR, "block": SCALE_BLOCK128}
 STATUS = {0: "GIFT_OK", 1: "GIFT_ERR_INVALID_ARG", 2: "GIFT_ERR_WORKSPACE", 3: "GIFT_ERR_NOT_READY",
@@ -54,6 +56,8 @@ EXPORTS = [
     "gift_group_encode", "gift_group_decode_reduce",
     "gift_act_scale_bytes", "gift_act_save", "gift_act_restore", "gift_norm_forward", "gift_norm_workspace_bytes",
     "gift_norm_backward", "gift_weight_grad_workspace_bytes", "gift_weight_grad",
+    "gift_weight_grad_x_workspace_bytes", "gift_weight_grad_x", "gift_dropout_apply", "gift_glu_workspace_bytes",
+    "gift_glu_forward", "gift_glu_backward_workspace_bytes", "gift_glu_backward",
 ]
 
 
@@ -73,6 +77,11 @@ class LayerDesc(ctypes.Structure):
 class ActCkpt(ctypes.Structure):
     _fields_ = [("d_codes", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("d_bscales", ctypes.c_void_p),
                 ("fmt", ctypes.c_int32)]
+
+
+class DropoutDesc(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("d_offset", ctypes.c_void_p)]
 
 
 _vp, _sz, _i32, _i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
@@ -139,6 +148,15 @@ _sig("gift_norm_backward", _i32, _i32, _vp, _i32, _i64, _vp, _i64, _P(ActCkpt), 
      _i64, _vp, _vp, _i32, _vp, _sz, _vp)
 _sig("gift_weight_grad_workspace_bytes", _sz, _i64, _i32, _i32, _i32)
 _sig("gift_weight_grad", _i32, _vp, _i32, _i64, _i32, _P(ActCkpt), _i64, _i32, _f32, _i32, _vp, _i64, _vp, _sz, _vp)
+_sig("gift_weight_grad_x_workspace_bytes", _sz, _i64, _i32, _i32, _i32, _i32)
+_sig("gift_weight_grad_x", _i32, _vp, _i32, _i64, _i32, _vp, _i64, _i64, _i32, _f32, _i32, _vp, _i64, _vp, _sz, _vp)
+_sig("gift_dropout_apply", _i32, _P(DropoutDesc), _vp, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp)
+_sig("gift_glu_workspace_bytes", _sz, _i64, _i32, _i32, _i32, _i32)
+_sig("gift_glu_forward", _i32, _i32, _vp, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _P(DropoutDesc), _vp,
+     _i64, _vp, _i64, _vp, _i64, _P(ActCkpt), _vp, _sz, _vp)
+_sig("gift_glu_backward_workspace_bytes", _sz, _i64, _i32, _i32, _i32, _i32)
+_sig("gift_glu_backward", _i32, _i32, _vp, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _P(DropoutDesc), _vp, _i64,
+     _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _sz, _vp)
 
 
 def set_fused(enable: bool) -> bool:
@@ -551,7 +569,7 @@ class Group:
             pass
 
 
-# -- activation operators (gift_act_*, gift_norm_*, gift_weight_grad) -----------
+# -- activation operators (gift_act_*, gift_norm_*, gift_weight_grad*) -----------
 # What these functions allocate (outputs not given, workspaces) comes from the
 # allocator's pool of the stream they launch on, so it may be dropped as soon
 # as the call returns; tensors the caller passes are the caller's to order.
@@ -772,27 +790,203 @@ def norm_backward(dy: torch.Tensor, x, mean, rstd, weight=None, kind="layer", dx
     return dx, dweight, dbias
 
 
-def weight_grad(delta: torch.Tensor, ckpt: ActCheckpoint, alpha: float = 1.0, out=None, accumulate: bool = False,
-                work=None, stream=None) -> torch.Tensor:
+def weight_grad(delta: torch.Tensor, ckpt, alpha: float = 1.0, out=None, accumulate: bool = False, work=None,
+                stream=None) -> torch.Tensor:
     """alpha delta^T a [m][d] in fp32 (plus `out` when accumulate), from the
-    output gradients delta [T][m] and the checkpoint of the layer's input a
-    [T][d]: the gradient Layer.encode takes."""
-    T, d = ckpt.T, ckpt.d
+    output gradients delta [T][m] and the layer's input a [T][d], either its
+    checkpoint or the tensor itself (of delta's type): the gradient
+    Layer.encode takes."""
+    whole = not isinstance(ckpt, ActCheckpoint)
+    if whole:
+        ldx = _rows(ckpt, "the activation", None, None, delta.dtype)
+        T, d = ckpt.shape
+    else:
+        T, d = ckpt.T, ckpt.d
     ld = _rows(delta, "delta", T)
     m, dev, dt = delta.shape[1], delta.device, DTYPES[delta.dtype]
     raw = _raw_stream(stream, dev)
-    _on(dev, ckpt, "the checkpoint")
+    _on(dev, ckpt, "the activation" if whole else "the checkpoint")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the tensor to add to")
         out, ldw = _empty(stream, (m, d), torch.float32, dev), d
     else:
         ldw = _rows(out, "out", m, d, torch.float32, dev)
-    if work is None:
-        work = _empty(stream, (_lib.gift_weight_grad_workspace_bytes(T, m, d, dt),), torch.uint8, dev)
-        wbytes = work.numel()
+    if whole:
+        dp, xp = delta.data_ptr(), ckpt.data_ptr()
+        wbytes = _lib.gift_weight_grad_x_workspace_bytes(T, m, d, dt, _rows16(dt, (dp, ld, T), (xp, ldx, T)))
     else:
-        wbytes = _bytes(dev, work, "work")
-    _check(_lib.gift_weight_grad(delta.data_ptr(), dt, ld, m, ckpt._ref, T, d, alpha, int(accumulate), out.data_ptr(),
-                                 ldw, work.data_ptr(), wbytes, raw), "gift_weight_grad")
+        wbytes = _lib.gift_weight_grad_workspace_bytes(T, m, d, dt)
+    work, wp, wbytes = _workspace(stream, work, wbytes, dev)
+    if whole:
+        _check(_lib.gift_weight_grad_x(dp, dt, ld, m, xp, ldx, T, d, alpha, int(accumulate), out.data_ptr(), ldw, wp,
+                                       wbytes, raw), "gift_weight_grad_x")
+    else:
+        _check(_lib.gift_weight_grad(delta.data_ptr(), dt, ld, m, ckpt._ref, T, d, alpha, int(accumulate),
+                                     out.data_ptr(), ldw, wp, wbytes, raw), "gift_weight_grad")
     return out
+
+
+# -- gated feed-forward block and dropout (gift_glu_*, gift_dropout_apply) ------
+
+def _rows16(dt, *rows):
+    """Whether all matrices (address, leading dimension, rows) have 16-byte aligned rows."""
+    size = 4 if dt == FP32 else 2
+    for p, ld, n in rows:
+        if p % 16 or (n > 1 and ld * size % 16):
+            return 0
+    return 1
+
+
+def _workspace(stream, work, nbytes, device):
+    """The given workspace, or a new one of nbytes (none for 0): tensor, address, bytes."""
+    if work is not None:
+        return work, work.data_ptr(), _bytes(device, work, "work")
+    if nbytes == 0:
+        return None, None, 0
+    work = _empty(stream, (nbytes,), torch.uint8, device)
+    return work, work.data_ptr(), nbytes
+
+
+def _act(act):
+    code = ACTS.get(act, act)
+    if code not in ACTS.values():
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, not {act!r}")
+    return code
+
+
+class Dropout:
+    """Dropout of probability p (counted in steps of 2^-16) whose mask is a
+    function of an element's place, `seed` and the offset: nothing is stored,
+    the backward pass takes the same Dropout.  The offset is `offset` plus,
+    when `counter` is given, the number in that one-element int64 GPU tensor,
+    read when the kernel runs: a captured graph draws another mask at each
+    replay if the counter is increased between them.  Uses that are to draw
+    apart need different seeds or offsets."""
+
+    _FIXED = frozenset(("p", "seed", "offset", "counter"))
+
+    def __init__(self, p: float, seed: int, offset: int = 0, counter=None):
+        p, seed, offset = float(p), int(seed), int(offset)
+        if not 0.0 <= p <= 1.0 or not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
+            raise ValueError("dropout needs 0 <= p <= 1 and a seed and an offset of 64 bits")
+        if counter is not None and (counter.dtype != torch.int64 or counter.numel() != 1 or not counter.is_cuda):
+            raise ValueError("counter must be an int64 tensor of one element on the GPU")
+        c = DropoutDesc(p, seed, offset, None if counter is None else counter.data_ptr())
+        self.__dict__.update(p=p, seed=seed, offset=offset, counter=counter, _c=c, _ref=ctypes.byref(c))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED:
+            raise AttributeError(f"a dropout's {name} cannot be replaced")
+        super().__setattr__(name, value)
+
+
+def _drop(drop, device):
+    if drop is None:
+        return None
+    if drop.counter is not None:
+        _on(device, drop.counter, "the dropout's counter")
+    return drop._ref
+
+
+def dropout_forward(x: torch.Tensor, drop: Dropout, residual=None, out=None, stream=None) -> torch.Tensor:
+    """Dropout of x [T][d], plus `residual` [T][d] when given.  `out` may be x or the residual."""
+    ld = _rows(x, "x")
+    (T, d), dev, dt = x.shape, x.device, x.dtype
+    raw = _raw_stream(stream, dev)
+    ref = _drop(drop, dev)
+    ldr, rp = (0, None) if residual is None else (_rows(residual, "residual", T, d, dt, dev), residual.data_ptr())
+    if out is None:
+        out, ldo = _empty_like(stream, x), d
+    else:
+        ldo = _rows(out, "out", T, d, dt, dev)
+    _check(_lib.gift_dropout_apply(ref, x.data_ptr(), DTYPES[dt], ld, T, d, rp, ldr, out.data_ptr(), ldo, raw),
+           "gift_dropout_apply")
+    return out
+
+
+def dropout_backward(dy: torch.Tensor, drop: Dropout, dx=None, stream=None) -> torch.Tensor:
+    """Gradient of dropout_forward's x from that of its output (the residual's is dy itself)."""
+    return dropout_forward(dy, drop, out=dx, stream=stream)
+
+
+def glu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act="silu", keep: bool = False, drop=None,
+                ckpt=None, out=None, gate=None, up=None, work=None, stream=None):
+    """Gated feed-forward block: h = drop(act(x w_gate^T) (x w_up^T)) [T][f],
+    for x [T][d] and weights [f][d] of its type (separate, or halves of one
+    matrix).  Returns h, gate and up: with `keep` (or given tensors) the two
+    products, for glu_backward, else None.  With `ckpt` (an ActCheckpoint
+    [T][f]) h is also saved there."""
+    act = _act(act)
+    ld = _rows(x, "x")
+    (T, d), dev, dt = x.shape, x.device, x.dtype
+    raw = _raw_stream(stream, dev)
+    ldg, f = _rows(w_gate, "w_gate", None, d, dt, dev), w_gate.shape[0]
+    ldu = _rows(w_up, "w_up", f, d, dt, dev)
+    ref = _drop(drop, dev)
+    if ckpt is not None:
+        if (ckpt.T, ckpt.d) != (T, f):
+            raise ValueError("the checkpoint has another shape than h")
+        _on(dev, ckpt, "the checkpoint")
+    if out is None:
+        out, ldh = _empty(stream, (T, f), dt, dev), f
+    else:
+        ldh = _rows(out, "out", T, f, dt, dev)
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up are given together")
+    if gate is not None:
+        ldz, ldup = _rows(gate, "gate", T, f, dt, dev), _rows(up, "up", T, f, dt, dev)
+    elif keep:
+        gate, up, ldz, ldup = _empty(stream, (T, f), dt, dev), _empty(stream, (T, f), dt, dev), f, f
+    else:
+        ldz = ldup = 0
+    t, xp, gp, wp = DTYPES[dt], x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+    work, kp, wbytes = _workspace(stream, work, _lib.gift_glu_workspace_bytes(
+        T, d, f, t, _rows16(t, (xp, ld, T), (gp, ldg, f), (wp, ldu, f))), dev)
+    _check(_lib.gift_glu_forward(act, xp, t, ld, T, d, gp, ldg, wp, ldu, f, ref, out.data_ptr(), ldh,
+                                 None if gate is None else gate.data_ptr(), ldz, None if up is None else up.data_ptr(),
+                                 ldup, None if ckpt is None else ckpt._ref, kp, wbytes, raw), "gift_glu_forward")
+    return out, gate, up
+
+
+def glu_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, w_gate=None, w_up=None, act="silu", drop=None,
+                 dx=None, dgate=None, dup=None, work=None, stream=None):
+    """Backward of glu_forward from dh [T][f] and what it kept.  Returns dx
+    [T][d] (None without the weights), and the gradients of both products,
+    dgate and dup [T][f], which weight_grad takes (given as the halves of one
+    [T][2 f] tensor, one weight_grad makes the gradient of both weights).
+    dgate and dup may be gate, up or dh."""
+    act = _act(act)
+    ld = _rows(dh, "dh")
+    (T, f), dev, dt = dh.shape, dh.device, dh.dtype
+    raw = _raw_stream(stream, dev)
+    ldz, ldup = _rows(gate, "gate", T, f, dt, dev), _rows(up, "up", T, f, dt, dev)
+    ref = _drop(drop, dev)
+    if (w_gate is None) != (w_up is None) or (w_gate is None and dx is not None):
+        raise ValueError("dx needs both weights")
+    if dgate is None:
+        dgate, lddz = _empty(stream, (T, f), dt, dev), f
+    else:
+        lddz = _rows(dgate, "dgate", T, f, dt, dev)
+    if dup is None:
+        dup, lddup = _empty(stream, (T, f), dt, dev), f
+    else:
+        lddup = _rows(dup, "dup", T, f, dt, dev)
+    t, zp, up_ = DTYPES[dt], dgate.data_ptr(), dup.data_ptr()
+    if w_gate is None:
+        d = ldg = ldu = lddx = nbytes = 0
+        gp = wp = xp = None
+    else:
+        ldg, d = _rows(w_gate, "w_gate", f, None, dt, dev), w_gate.shape[1]
+        ldu = _rows(w_up, "w_up", f, d, dt, dev)
+        if dx is None:
+            dx, lddx = _empty(stream, (T, d), dt, dev), d
+        else:
+            lddx = _rows(dx, "dx", T, d, dt, dev)
+        gp, wp, xp = w_gate.data_ptr(), w_up.data_ptr(), dx.data_ptr()
+        nbytes = _lib.gift_glu_backward_workspace_bytes(
+            T, d, f, t, _rows16(t, (zp, lddz, T), (up_, lddup, T), (gp, ldg, f), (wp, ldu, f)))
+    work, kp, wbytes = _workspace(stream, work, nbytes, dev)
+    _check(_lib.gift_glu_backward(act, dh.data_ptr(), t, ld, T, f, gate.data_ptr(), ldz, up.data_ptr(), ldup, ref, zp,
+                                  lddz, up_, lddup, gp, ldg, wp, ldu, d, xp, lddx, kp, wbytes, raw), "gift_glu_backward")
+    return dx, dgate, dup

@@ -292,6 +292,57 @@ int64_t wgrad_grid(int m, int d);
 size_t wgrad_workspace(int64_t T, int m, int d, int dtype);
 hipError_t launch_weight_grad(const WgradCall& c, hipStream_t s);
 
+// Gated feed-forward block, dropout, weight gradient from a whole activation
+// (k_glu.hip, k_dropout.hip).
+struct DropArgs;
+struct GluCall {
+  int act, dtype;
+  const void* x;
+  int64_t ldx, T;
+  int d, f;
+  const void *wg, *wu;
+  int64_t ldg, ldu;
+  void *h, *gate, *up;
+  int64_t ldh, ldz, ldup;
+  const gift_act_ckpt* ckpt;
+  void* work;
+};
+struct GluGradCall {
+  int act, dtype;
+  const void *dh, *gate, *up;
+  int64_t lddh, ldz, ldup, T;
+  int d, f;
+  void *dgate, *dup;
+  int64_t lddz, lddup;
+  const void *wg, *wu;
+  int64_t ldg, ldu;
+  void* dx;
+  int64_t lddx;
+  void* work;
+};
+struct WgradXCall {
+  const void* delta;
+  int dtype;
+  int64_t ldd;
+  int m;
+  const void* x;
+  int64_t ldx, T;
+  int d;
+  float alpha;
+  int accumulate;
+  float* W;
+  int64_t ldw;
+  void* work;
+};
+int64_t dropout_grid(int64_t T, int d);
+hipError_t launch_dropout(const DropArgs& drop, const void* x, int dtype, int64_t ldx, int64_t T, int d, const void* r,
+                          int64_t ldr, void* y, int64_t ldy, hipStream_t s);
+int64_t glu_grid(int64_t T, int n);
+int64_t glu_gradients_grid(int64_t T, int f);
+hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s);
+hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s);
+hipError_t launch_wgrad_x(const WgradXCall& c, hipStream_t s);
+
 hipError_t launch_amax_out(const uint32_t* slots, float* amax_out, int64_t n, hipStream_t s);
 hipError_t launch_amax_flat(const float* g, int64_t n, uint32_t* slot, hipStream_t s);
 

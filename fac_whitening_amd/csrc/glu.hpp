@@ -1,0 +1,82 @@
+// Shared device code of the gated feed-forward block and of dropout: the
+// counter-based generator and the activations.
+#pragma once
+#include "act8.hpp"
+
+namespace gift {
+
+// Dropout as the kernels take it.  thr = round(65536 p); on == 0: no dropout.
+struct DropArgs {
+  uint32_t thr;
+  float scale;
+  uint32_t k0, k1;             // seed
+  uint64_t offset;
+  const uint64_t* d_offset;
+  int on;
+};
+
+// Philox4x32-10 (Salmon et al., SC 2011): ten rounds of two 32 x 32 -> 64 bit
+// products by fixed odd numbers, mixed with a key that grows by fixed steps.
+__device__ __forceinline__ void philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1,
+                                       uint32_t* w) {
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)b;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  w[0] = c0;
+  w[1] = c1;
+  w[2] = c2;
+  w[3] = c3;
+}
+
+__device__ __forceinline__ uint64_t drop_offset(const DropArgs& a) {
+  return a.offset + (a.d_offset ? *a.d_offset : 0);
+}
+
+// Bits of columns 8 chunk .. 8 chunk + 7 of row t, 16 each, two to a word.
+__device__ __forceinline__ void drop_bits(const DropArgs& a, uint64_t offset, uint32_t t, uint32_t chunk, uint32_t* w) {
+  philox(chunk, t, (uint32_t)offset, (uint32_t)(offset >> 32), a.k0, a.k1, w);
+}
+__device__ __forceinline__ float drop_one(const DropArgs& a, const uint32_t* w, int i, float v) {
+  const uint32_t r = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+  return r >= a.thr ? v * a.scale : 0.f;
+}
+
+// act(z) and, where asked for, act'(z).  In fp32 with the library's exp and
+// erfc: an fp32 result is to hold its last bits.
+template <int ACT>
+__device__ __forceinline__ float act_value(float z, float* grad = nullptr) {
+  if constexpr (ACT == GIFT_ACT_RELU) {
+    if (grad) *grad = z > 0.f ? 1.f : z == z ? 0.f : z;
+    return z > 0.f ? z : z == z ? 0.f : z;
+  } else if constexpr (ACT == GIFT_ACT_SILU || ACT == GIFT_ACT_SIGMOID) {
+    const float e = expf(-__builtin_fabsf(z)), r = 1.f / (1.f + e);
+    const float s = z >= 0.f ? r : e * r, q = z >= 0.f ? e * r : r;   // s(z) and s(-z)
+    if constexpr (ACT == GIFT_ACT_SIGMOID) {
+      if (grad) *grad = s * q;
+      return s;
+    } else {
+      if (grad) *grad = s * (1.f + z * q);
+      return z * s;
+    }
+  } else if constexpr (ACT == GIFT_ACT_GELU) {
+    const float n = 0.5f * erfcf(-0.70710678118654752f * z);
+    if (grad) *grad = n + z * (0.3989422804014327f * expf(-0.5f * z * z));
+    return z * n;
+  } else {
+    constexpr float k = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+    const float w = k * (z + 0.044715f * z * z * z);
+    const float e = expf(-__builtin_fabsf(w)), r = 1.f / (1.f + e);
+    const float s = w >= 0.f ? r : e * r, q = w >= 0.f ? e * r : r;
+    if (grad) *grad = s + z * s * q * (k * (1.f + 0.134145f * z * z));
+    return z * s;
+  }
+}
+
+}  // namespace gift

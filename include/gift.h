@@ -413,6 +413,7 @@ gift_status gift_group_decode_reduce(gift_group_t group, gift_stream_t stream);
  *   gift_norm_forward / _backward      layer norm and RMS norm; the forward can keep its input as a
  *                                      checkpoint, the backward can read it instead of the input
  *   gift_weight_grad                   W = alpha delta^T a from the checkpoint of a, fp32: gift_encode's input
+ *   gift_weight_grad_x                 the same from an activation kept whole
  *
  * They are stateless (no handle) and may be called from any thread.  Element
  * types are GIFT_BF16, GIFT_FP16 and GIFT_FP32.  Unlike the calls above, rows
@@ -494,6 +495,74 @@ size_t gift_weight_grad_workspace_bytes(int64_t T, int32_t m, int32_t d, int32_t
 gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, int32_t m, const gift_act_ckpt* h_ckpt,
                              int64_t T, int32_t d, float alpha, int32_t accumulate, float* d_W, int64_t ldw,
                              void* d_work, size_t work_bytes, gift_stream_t stream);
+
+/* W = alpha delta^T x (+ W when accumulate != 0) as gift_weight_grad, from an activation x [T][ldx] of delta's type
+ * that was kept whole.  bf16 and fp16 products are exact in the fp32 sums.  An fp32 operand is the sum of three bf16
+ * numbers, of whose nine products the six largest are added: what is left out is below 2^-24 of |delta| |x|; an
+ * infinity in an fp32 operand gives NaN.  Sums are fp32, in the same order on every call.
+ * d_W may not overlap delta or x. */
+size_t gift_weight_grad_x_workspace_bytes(int64_t T, int32_t m, int32_t d, int32_t dtype, int32_t aligned);
+gift_status gift_weight_grad_x(const void* d_delta, int32_t dtype, int64_t ldd, int32_t m, const void* d_x,
+                               int64_t ldx, int64_t T, int32_t d, float alpha, int32_t accumulate, float* d_W,
+                               int64_t ldw, void* d_work, size_t work_bytes, gift_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated feed-forward block and dropout: what makes the input a of the layer
+ * whose gradient is encoded ([Note] §实验设置: Llama-class MLP layers, fc2).
+ * The conventions of the activation operators above hold here too.
+ *
+ * Dropout keeps nothing: whether element (t, j) of a matrix is kept is a
+ * function of its place and of three numbers,
+ *   keep(t, j) = bits(t, j) >= thr,  thr = round(65536 p)  (p = 0: all are kept)
+ *   D(x) = keep ? x 65536 / (65536 - thr) : 0
+ * so p counts in steps of 2^-16.  bits are half j % 2 of word (j % 8) / 2 of
+ * Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3",
+ * SC 2011) at the counter (j / 8, t, low and high word of the offset) under
+ * the key (low and high word of the seed).  The offset is `offset` plus, when
+ * d_offset is given, the number there (8-byte aligned device memory, read
+ * when the kernel runs, so that replays of a captured graph may draw other masks).
+ * Calls that are to draw apart need different offsets or seeds.  T <= 2^32.
+ * ------------------------------------------------------------------------- */
+typedef struct gift_dropout {
+  double p;                 /* 0 .. 1 */
+  uint64_t seed, offset;
+  const uint64_t* d_offset; /* may be NULL */
+} gift_dropout;
+/* y = D(x) (+ residual when given) in fp32, rounded once to `dtype`.  The backward pass is the same call on dy,
+ * without a residual.  d_y may be d_x or d_residual, with the same leading dimension; any other overlap is refused. */
+gift_status gift_dropout_apply(const gift_dropout* h_drop, const void* d_x, int32_t dtype, int64_t ldx, int64_t T,
+                               int32_t d, const void* d_residual, int64_t ldr, void* d_y, int64_t ldy,
+                               gift_stream_t stream);
+
+/* Gated feed-forward block, x [T][d], Wg and Wu [f][d] (halves of one [2 f][d] matrix or separate):
+ *   z = x Wg^T, u = x Wu^T, h = D(act(z) u)
+ * act(z): silu z s(z), gelu z N(z) (N the normal distribution function), gelu_tanh z s(2 sqrt(2 / pi) (z + 0.044715
+ * z^3)), relu max(z, 0), sigmoid s(z), with s(z) = 1 / (1 + e^-z). */
+enum gift_act { GIFT_ACT_SILU = 0, GIFT_ACT_GELU = 1, GIFT_ACT_GELU_TANH = 2, GIFT_ACT_RELU = 3, GIFT_ACT_SIGMOID = 4 };
+/* h, from the fp32 sums z and u, is rounded once to `dtype`.  d_gate, d_up [T][f] (both or neither): z and u rounded
+ * to `dtype`, for the backward pass.  h_drop: NULL for none.  h_ckpt: h [T][f] as it was rounded is also saved there.
+ * Outputs may overlap neither an input nor each other.  fp32 products as in gift_weight_grad_x.
+ * d_work: 16-byte aligned, gift_glu_workspace_bytes; `aligned` there is nonzero when
+ * d_x, d_wg and d_wu and their rows are 16-byte aligned (else the call first lays them out anew in the workspace). */
+size_t gift_glu_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t dtype, int32_t aligned);
+gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_t ldx, int64_t T, int32_t d,
+                             const void* d_wg, int64_t ldg, const void* d_wu, int64_t ldu, int32_t f,
+                             const gift_dropout* h_drop, void* d_h, int64_t ldh, void* d_gate, int64_t ldz, void* d_up,
+                             int64_t ldup, const gift_act_ckpt* h_ckpt, void* d_work, size_t work_bytes,
+                             gift_stream_t stream);
+/* From dh [T][f] and what the forward kept, with e = D(dh):
+ *   dgate = e u act'(z), dup = e act(z),  dx = dgate Wg + dup Wu   (relu'(0) = 0)
+ * dgate and dup are rounded to `dtype`, and dx [T][d] is the product of the rounded values: they are the operands of
+ * the weight gradients (gift_weight_grad, gift_weight_grad_x) too.  d_dx NULL: dgate and dup only (the weights and
+ * the workspace are not used).  dgate and dup may each be dh, gate or up, with the same leading dimension; any other
+ * overlap with them, of each other, or of dx with dgate, dup or the weights is refused.
+ * `aligned`: of dgate, dup, Wg and Wu. */
+size_t gift_glu_backward_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t dtype, int32_t aligned);
+gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int64_t lddh, int64_t T, int32_t f,
+                              const void* d_gate, int64_t ldz, const void* d_up, int64_t ldup,
+                              const gift_dropout* h_drop, void* d_dgate, int64_t lddz, void* d_dup, int64_t lddup,
+                              const void* d_wg, int64_t ldg, const void* d_wu, int64_t ldu, int32_t d, void* d_dx,
+                              int64_t lddx, void* d_work, size_t work_bytes, gift_stream_t stream);
 
 /* Scale-sync schedule ([Note] Algorithm 1, its scale-sync step): the geometry-aware
  * layers quantise with their local scale and, on a scale-sync step, with the
