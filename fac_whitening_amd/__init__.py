@@ -830,10 +830,10 @@ def weight_grad(delta: torch.Tensor, ckpt, alpha: float = 1.0, out=None, accumul
 # -- gated feed-forward block and dropout (gift_glu_*, gift_dropout_apply) ------
 
 def _rows16(dt, *rows):
-    """Whether all matrices (address, leading dimension, rows) have 16-byte aligned rows."""
+    """Whether all matrices (address, leading dimension, rows) have 16-byte aligned rows, at most 4 MB apart."""
     size = 4 if dt == FP32 else 2
     for p, ld, n in rows:
-        if p % 16 or (n > 1 and ld * size % 16):
+        if p % 16 or (n > 1 and (ld * size % 16 or ld * size > 1 << 22)):
             return 0
     return 1
 
@@ -985,7 +985,8 @@ def glu_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, w_gate=
             lddx = _rows(dx, "dx", T, d, dt, dev)
         gp, wp, xp = w_gate.data_ptr(), w_up.data_ptr(), dx.data_ptr()
         nbytes = _lib.gift_glu_backward_workspace_bytes(
-            T, d, f, t, _rows16(t, (zp, lddz, T), (up_, lddup, T), (gp, ldg, f), (wp, ldu, f)))
+            T, d, f, t, int((lddz == lddup or T == 1) and (ldg == ldu or f == 1) and
+                            _rows16(t, (zp, lddz, T), (up_, lddup, T), (gp, ldg, f), (wp, ldu, f))))
     work, kp, wbytes = _workspace(stream, work, nbytes, dev)
     _check(_lib.gift_glu_backward(act, dh.data_ptr(), t, ld, T, f, gate.data_ptr(), ldz, up.data_ptr(), ldup, ref, zp,
                                   lddz, up_, lddup, gp, ldg, wp, ldu, d, xp, lddx, kp, wbytes, raw), "gift_glu_backward")

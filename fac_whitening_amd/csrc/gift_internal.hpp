@@ -305,6 +305,7 @@ struct GluCall {
   void *h, *gate, *up;
   int64_t ldh, ldz, ldup;
   const gift_act_ckpt* ckpt;
+  bool aligned;         // rows of x and the weights (see ProdOperand)
   void* work;
 };
 struct GluGradCall {
@@ -318,6 +319,7 @@ struct GluGradCall {
   int64_t ldg, ldu;
   void* dx;
   int64_t lddx;
+  bool aligned;         // rows of dgate, dup and the weights; both of each the same distance apart
   void* work;
 };
 struct WgradXCall {
@@ -332,13 +334,16 @@ struct WgradXCall {
   int accumulate;
   float* W;
   int64_t ldw;
+  bool aligned;         // rows of delta and x
   void* work;
 };
 int64_t dropout_grid(int64_t T, int d);
 hipError_t launch_dropout(const DropArgs& drop, const void* x, int dtype, int64_t ldx, int64_t T, int d, const void* r,
                           int64_t ldr, void* y, int64_t ldy, hipStream_t s);
-int64_t glu_grid(int64_t T, int n);
 int64_t glu_gradients_grid(int64_t T, int f);
+size_t glu_forward_workspace(const GluCall& c);
+size_t glu_backward_workspace(const GluGradCall& c);
+size_t wgrad_x_workspace(const WgradXCall& c);
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_wgrad_x(const WgradXCall& c, hipStream_t s);

@@ -48,15 +48,22 @@ __device__ __forceinline__ float drop_one(const DropArgs& a, const uint32_t* w, 
   return r >= a.thr ? v * a.scale : 0.f;
 }
 
-// act(z) and, where asked for, act'(z).  In fp32 with the library's exp and
-// erfc: an fp32 result is to hold its last bits.
+// act(z) and, where asked for, act'(z), in fp32: every factor relative to its
+// own size, also where act tends to zero.  exp2 and the reciprocal are the
+// hardware's (1 ulp each); e^-v as 2^(-v log2 e) is off by v 2^-24 of itself.
+// The normal distribution's tail is e^(-z^2 / 2) q(t), t = 1 / (1 + |z| / (2
+// sqrt 2)): q is a polynomial fitted to it over |z| <= 14.8, below which e^(-z^2 /
+// 2) ends, off by 3.4e-8 of the tail at most.
+__device__ __forceinline__ float exp_neg(float v) { return __builtin_amdgcn_exp2f(v * -1.4426950408889634f); }
+__device__ __forceinline__ float reciprocal(float v) { return __builtin_amdgcn_rcpf(v); }
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z, float* grad = nullptr) {
   if constexpr (ACT == GIFT_ACT_RELU) {
     if (grad) *grad = z > 0.f ? 1.f : z == z ? 0.f : z;
     return z > 0.f ? z : z == z ? 0.f : z;
   } else if constexpr (ACT == GIFT_ACT_SILU || ACT == GIFT_ACT_SIGMOID) {
-    const float e = expf(-__builtin_fabsf(z)), r = 1.f / (1.f + e);
+    const float e = exp_neg(__builtin_fabsf(z)), r = reciprocal(1.f + e);
     const float s = z >= 0.f ? r : e * r, q = z >= 0.f ? e * r : r;   // s(z) and s(-z)
     if constexpr (ACT == GIFT_ACT_SIGMOID) {
       if (grad) *grad = s * q;
@@ -66,15 +73,27 @@ __device__ __forceinline__ float act_value(float z, float* grad = nullptr) {
       return z * s;
     }
   } else if constexpr (ACT == GIFT_ACT_GELU) {
-    const float n = 0.5f * erfcf(-0.70710678118654752f * z);
-    if (grad) *grad = n + z * (0.3989422804014327f * expf(-0.5f * z * z));
+    const float e = exp_neg(0.5f * z * z);
+    const float t = reciprocal(1.f + 0.35355339059327373f * __builtin_fabsf(z));
+    float q = -0.0279172214f;
+    q = q * t + 0.133988569f;
+    q = q * t - 0.225301468f;
+    q = q * t + 0.116354035f;
+    q = q * t + 0.00403949032f;
+    q = q * t + 0.0928747958f;
+    q = q * t + 0.124178955f;
+    q = q * t + 0.140689721f;
+    q = q * t + 0.14109541f;
+    q = q * t - 2.30335438e-06f;
+    const float tail = q * e, n = z >= 0.f ? 1.f - tail : tail;
+    if (grad) *grad = n + z * (0.3989422804014327f * e);
     return z * n;
   } else {
     constexpr float k = 1.5957691216057308f;   // 2 sqrt(2 / pi)
     const float w = k * (z + 0.044715f * z * z * z);
-    const float e = expf(-__builtin_fabsf(w)), r = 1.f / (1.f + e);
+    const float e = exp_neg(__builtin_fabsf(w)), r = reciprocal(1.f + e);
     const float s = w >= 0.f ? r : e * r, q = w >= 0.f ? e * r : r;
-    if (grad) *grad = s + z * s * q * (k * (1.f + 0.134145f * z * z));
+    if (grad) *grad = s + z * (s * q) * (k * (1.f + 0.134145f * z * z));
     return z * s;
   }
 }

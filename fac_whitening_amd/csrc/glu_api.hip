@@ -4,7 +4,7 @@
 #include <cmath>
 #include <numeric>
 
-#include "glu.hpp"
+#include "product.hpp"
 
 namespace {
 
@@ -23,7 +23,10 @@ struct Matrix {
   int64_t ld, rows;
   int64_t cols, size;
   bool ok() const { return rows == 0 || (p && aligned_to(p, (size_t)size) && ld >= cols); }
-  bool rows16() const { return aligned_to(p, 16) && (rows <= 1 || ld * size % 16 == 0); }
+  // as the products read it (see gift_glu_workspace_bytes)
+  bool rows16() const {
+    return aligned_to(p, 16) && (rows <= 1 || (ld * size % 16 == 0 && ld * size <= gift::kProductRow));
+  }
   __int128 begin() const { return (__int128)reinterpret_cast<uintptr_t>(p); }
   __int128 end() const { return begin() + ((__int128)(rows - 1) * ld + cols) * size; }
 };
@@ -68,6 +71,14 @@ gift::DropArgs drop_args(const gift_dropout* d) {
 }
 constexpr int64_t kDropRows = (int64_t)1 << 32;
 
+// What a product's launches reach: columns whose rows the kernel's 32-bit offsets span, tiles of the output, and rows
+// that may have to be laid out anew.
+constexpr int kProductCols = (int)(gift::kProductRow / 2);
+bool reach(int64_t M, int64_t N, int64_t rows, int64_t cols) {
+  return M <= kProductCols && rows < ((int64_t)1 << 36) && gift::product_tiles(M, N) <= kMaxGrid &&
+         rows <= kMaxGrid * 256 / gift::cdiv(cols, 8);
+}
+
 bool act_ok(int32_t a) { return a >= GIFT_ACT_SILU && a <= GIFT_ACT_SIGMOID; }
 gift_status result(hipError_t e) { return e == hipSuccess ? GIFT_OK : gift::hip_failure(e); }
 
@@ -89,7 +100,15 @@ gift_status gift_dropout_apply(const gift_dropout* h_drop, const void* d_x, int3
 }
 
 size_t gift_glu_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t dtype, int32_t aligned) {
-  return 0;
+  if (!rows_count_ok(T) || !cols_ok(d) || !cols_ok(f) || !dtype_ok(dtype)) return 0;
+  if (d > kProductCols || !reach(f, T, T, d)) return 0;
+  gift::GluCall c{};
+  c.dtype = dtype;
+  c.T = T;
+  c.d = d;
+  c.f = f;
+  c.aligned = aligned != 0;
+  return gift::glu_forward_workspace(c);
 }
 
 gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_t ldx, int64_t T, int32_t d,
@@ -121,7 +140,7 @@ gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_
       if (!disjoint(out[k], out[l])) return GIFT_ERR_INVALID_ARG;
   }
   if (h_drop && T > kDropRows) return GIFT_ERR_UNSUPPORTED;
-  if (gift::glu_grid(T, f) > kMaxGrid || (h_ckpt && gift::act_grid(T, f) > kMaxGrid)) return GIFT_ERR_UNSUPPORTED;
+  if (d > kProductCols || !reach(f, T, T, d) || (h_ckpt && gift::act_grid(T, f) > kMaxGrid)) return GIFT_ERR_UNSUPPORTED;
   gift::GluCall c{};
   c.act = act;
   c.dtype = dtype;
@@ -141,7 +160,11 @@ gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_
   c.ldz = ldz;
   c.ldup = ldup;
   c.ckpt = h_ckpt;
+  c.aligned = x.rows16() && wg.rows16() && wu.rows16();
   c.work = d_work;
+  const size_t need = gift::glu_forward_workspace(c);
+  if (need && (!d_work || !aligned_to(d_work, 16))) return GIFT_ERR_INVALID_ARG;
+  if (work_bytes < need) return GIFT_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = gift::launch_glu_forward(c, drop_args(h_drop), s);
   if (e == hipSuccess && h_ckpt) e = gift::launch_act_save(d_h, dtype, ldh, T, f, *h_ckpt, s);
@@ -149,7 +172,15 @@ gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_
 }
 
 size_t gift_glu_backward_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t dtype, int32_t aligned) {
-  return 0;
+  if (!rows_count_ok(T) || !cols_ok(d) || !cols_ok(f) || !dtype_ok(dtype)) return 0;
+  if (f > kProductCols || !reach(d, T, T, f)) return 0;
+  gift::GluGradCall c{};
+  c.dtype = dtype;
+  c.T = T;
+  c.d = d;
+  c.f = f;
+  c.aligned = aligned != 0;
+  return gift::glu_backward_workspace(c);
 }
 
 gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int64_t lddh, int64_t T, int32_t f,
@@ -166,6 +197,7 @@ gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int6
   for (const Matrix& i : {dh, z, u})
     if (!in_place_or_disjoint(i, dz) || !in_place_or_disjoint(i, du)) return GIFT_ERR_INVALID_ARG;
   if (!disjoint(dz, du)) return GIFT_ERR_INVALID_ARG;
+  gift::GluGradCall c{};
   if (d_dx) {
     if (!cols_ok(d)) return GIFT_ERR_INVALID_ARG;
     const Matrix wg{d_wg, ldg, f, d, size}, wu{d_wu, ldu, f, d, size}, dx{d_dx, lddx, T, d, size};
@@ -173,10 +205,10 @@ gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int6
     for (const Matrix& i : {wg, wu})
       if (!disjoint(i, dx) || !disjoint(i, dz) || !disjoint(i, du)) return GIFT_ERR_INVALID_ARG;
     if (!disjoint(dz, dx) || !disjoint(du, dx)) return GIFT_ERR_INVALID_ARG;
-    if (gift::glu_grid(T, d) > kMaxGrid) return GIFT_ERR_UNSUPPORTED;
+    if (f > kProductCols || !reach(d, T, T, f)) return GIFT_ERR_UNSUPPORTED;
+    c.aligned = wg.rows16() && wu.rows16() && dz.rows16() && du.rows16() && (f == 1 || ldg == ldu) && (T == 1 || lddz == lddup);
   }
   if ((h_drop && T > kDropRows) || gift::glu_gradients_grid(T, f) > kMaxGrid) return GIFT_ERR_UNSUPPORTED;
-  gift::GluGradCall c{};
   c.act = act;
   c.dtype = dtype;
   c.dh = d_dh;
@@ -199,11 +231,24 @@ gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int6
   c.dx = d_dx;
   c.lddx = lddx;
   c.work = d_work;
+  if (d_dx) {
+    const size_t need = gift::glu_backward_workspace(c);
+    if (need && (!d_work || !aligned_to(d_work, 16))) return GIFT_ERR_INVALID_ARG;
+    if (work_bytes < need) return GIFT_ERR_WORKSPACE;
+  }
   return result(gift::launch_glu_backward(c, drop_args(h_drop), static_cast<hipStream_t>(stream)));
 }
 
 size_t gift_weight_grad_x_workspace_bytes(int64_t T, int32_t m, int32_t d, int32_t dtype, int32_t aligned) {
-  return 0;
+  if (!rows_count_ok(T) || !cols_ok(d) || !cols_ok(m) || !dtype_ok(dtype)) return 0;
+  if (m > kProductCols || !reach(d, m, T, d) || !reach(d, m, T, m)) return 0;
+  gift::WgradXCall c{};
+  c.dtype = dtype;
+  c.T = T;
+  c.m = m;
+  c.d = d;
+  c.aligned = aligned != 0;
+  return gift::wgrad_x_workspace(c);
 }
 
 gift_status gift_weight_grad_x(const void* d_delta, int32_t dtype, int64_t ldd, int32_t m, const void* d_x,
@@ -213,7 +258,7 @@ gift_status gift_weight_grad_x(const void* d_delta, int32_t dtype, int64_t ldd, 
   const int64_t size = dtype_size(dtype);
   const Matrix delta{d_delta, ldd, T, m, size}, x{d_x, ldx, T, d, size}, W{d_W, ldw, m, d, 4};
   if (!delta.ok() || !x.ok() || !W.ok() || !disjoint(delta, W) || !disjoint(x, W)) return GIFT_ERR_INVALID_ARG;
-  if (gift::glu_grid(m, d) > kMaxGrid) return GIFT_ERR_UNSUPPORTED;
+  if (m > kProductCols || !reach(d, m, T, d) || !reach(d, m, T, m)) return GIFT_ERR_UNSUPPORTED;
   gift::WgradXCall c{};
   c.delta = d_delta;
   c.dtype = dtype;
@@ -227,7 +272,11 @@ gift_status gift_weight_grad_x(const void* d_delta, int32_t dtype, int64_t ldd, 
   c.accumulate = accumulate ? 1 : 0;
   c.W = d_W;
   c.ldw = ldw;
+  c.aligned = delta.rows16() && x.rows16();
   c.work = d_work;
+  const size_t need = gift::wgrad_x_workspace(c);
+  if (need && (!d_work || !aligned_to(d_work, 16))) return GIFT_ERR_INVALID_ARG;
+  if (work_bytes < need) return GIFT_ERR_WORKSPACE;
   return result(gift::launch_wgrad_x(c, static_cast<hipStream_t>(stream)));
 }
 

@@ -4,102 +4,9 @@
 //   forward   z = x Wg^T, u = x Wu^T, h = D(act(z) u)
 //   backward  dgate = D(dh) u act'(z), dup = D(dh) act(z), dx = dgate Wg + dup Wu
 //   weights   W = alpha delta^T x
-//
-// First form, on the vector units: 64 x 64 outputs a workgroup, 4 x 4 a
-// thread, 32 of the long axis a stage, fp32 products and sums over 256,
-// folded into fp64.
-#include <type_traits>
-
-#include "glu.hpp"
+#include "product.hpp"
 
 namespace gift {
-
-__device__ __forceinline__ float value_of(const float* p) { return *p; }
-__device__ __forceinline__ float value_of(const Bf16* p) { return __uint_as_float((uint32_t)p->v << 16); }
-__device__ __forceinline__ float value_of(const Fp16* p) { return (float)__builtin_bit_cast(_Float16, p->v); }
-__device__ __forceinline__ void store_of(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_of(Bf16* p, float v) { p->v = __builtin_bit_cast(uint16_t, (__bf16)v); }
-__device__ __forceinline__ void store_of(Fp16* p, float v) { p->v = __builtin_bit_cast(uint16_t, (_Float16)v); }
-
-// Element (i, k) at p + i si + k sk.
-struct Operand {
-  const void* p;
-  int64_t si, sk;
-};
-
-// sum_k A(i0 + 4 ty + ., k) B(j0 + 4 tx + ., k) into sum (added).
-template <typename T>
-__device__ __forceinline__ void tile_product(const Operand& a, const Operand& b, int64_t i0, int64_t mi, int64_t j0, int64_t nj,
-                                             int64_t K, float (&A)[32][68], float (&B)[32][68], double (&sum)[4][4]) {
-  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += 32) {
-    __syncthreads();
-    for (int e = tid; e < 32 * 64; e += 256) {
-      // consecutive threads along the axis whose stride is one
-      const int ka = a.sk == 1 ? e % 32 : e / 64, ra = a.sk == 1 ? e / 32 : e % 64;
-      const int kb = b.sk == 1 ? e % 32 : e / 64, rb = b.sk == 1 ? e / 32 : e % 64;
-      A[ka][ra] = k0 + ka < K && i0 + ra < mi ? value_of(static_cast<const T*>(a.p) + (i0 + ra) * a.si + (k0 + ka) * a.sk) : 0.f;
-      B[kb][rb] = k0 + kb < K && j0 + rb < nj ? value_of(static_cast<const T*>(b.p) + (j0 + rb) * b.si + (k0 + kb) * b.sk) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll 4
-    for (int k = 0; k < 32; ++k) {
-      float p[4], q[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        p[x] = A[k][ty * 4 + x];
-        q[x] = B[k][tx * 4 + x];
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) acc[x][y] += p[x] * q[y];
-    }
-    if (((k0 / 32) & 7) == 7 || k0 + 32 >= K) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          sum[x][y] += (double)acc[x][y];
-          acc[x][y] = 0.f;
-        }
-    }
-  }
-}
-
-template <typename T, int ACT>
-__global__ void __launch_bounds__(256) k_glu_forward(GluCall c, DropArgs drop) {
-  __shared__ float A[32][68], B[32][68];
-  const int nbf = (c.f + 63) / 64;
-  const int64_t i0 = (int64_t)(blockIdx.x / nbf) * 64, j0 = (int64_t)(blockIdx.x % nbf) * 64;
-  double z[4][4] = {}, u[4][4] = {};
-  const Operand x{c.x, c.ldx, 1};
-  tile_product<T>(x, Operand{c.wg, c.ldg, 1}, i0, c.T, j0, c.f, c.d, A, B, z);
-  tile_product<T>(x, Operand{c.wu, c.ldu, 1}, i0, c.T, j0, c.f, c.d, A, B, u);
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const uint64_t offset = drop.on ? drop_offset(drop) : 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t t = i0 + ty * 4 + k;
-    if (t >= c.T) continue;
-    uint32_t w[4];
-    if (drop.on) drop_bits(drop, offset, (uint32_t)t, (uint32_t)(j0 + tx * 4) / 8, w);
-#pragma unroll
-    for (int l = 0; l < 4; ++l) {
-      const int64_t j = j0 + tx * 4 + l;
-      if (j >= c.f) continue;
-      const float zz = (float)z[k][l], uu = (float)u[k][l];
-      float h = act_value<ACT>(zz) * uu;
-      if (drop.on) h = drop_one(drop, w, (int)(j % 8), h);
-      store_of(static_cast<T*>(c.h) + t * c.ldh + j, h);
-      if (c.gate) {
-        store_of(static_cast<T*>(c.gate) + t * c.ldz + j, zz);
-        store_of(static_cast<T*>(c.up) + t * c.ldup + j, uu);
-      }
-    }
-  }
-}
 
 // dgate and dup: eight columns of a row a thread.
 template <typename T, int ACT>
@@ -135,45 +42,12 @@ __global__ void __launch_bounds__(256) k_glu_gradients(GluGradCall c, DropArgs d
   store8(static_cast<T*>(c.dup) + t * c.lddup + j, o, m, false);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_glu_dx(GluGradCall c) {
-  __shared__ float A[32][68], B[32][68];
-  const int nbd = (c.d + 63) / 64;
-  const int64_t i0 = (int64_t)(blockIdx.x / nbd) * 64, j0 = (int64_t)(blockIdx.x % nbd) * 64;
-  double s[4][4] = {};
-  tile_product<T>(Operand{c.dgate, c.lddz, 1}, Operand{c.wg, 1, c.ldg}, i0, c.T, j0, c.d, c.f, A, B, s);
-  tile_product<T>(Operand{c.dup, c.lddup, 1}, Operand{c.wu, 1, c.ldu}, i0, c.T, j0, c.d, c.f, A, B, s);
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-#pragma unroll
-    for (int l = 0; l < 4; ++l) {
-      const int64_t t = i0 + ty * 4 + k, j = j0 + tx * 4 + l;
-      if (t < c.T && j < c.d) store_of(static_cast<T*>(c.dx) + t * c.lddx + j, (float)s[k][l]);
-    }
+// W = 0: the gradient of no tokens.
+__global__ void __launch_bounds__(256) k_wgrad_none(float* W, int64_t ldw, int m, int d) {
+  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x, i = k / d;
+  if (i < m) W[i * ldw + (k - i * d)] = 0.f;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_wgrad_x(WgradXCall c) {
-  __shared__ float A[32][68], B[32][68];
-  const int nbd = (c.d + 63) / 64;
-  const int64_t i0 = (int64_t)(blockIdx.x / nbd) * 64, j0 = (int64_t)(blockIdx.x % nbd) * 64;
-  double s[4][4] = {};
-  tile_product<T>(Operand{c.delta, 1, c.ldd}, Operand{c.x, 1, c.ldx}, i0, c.m, j0, c.d, c.T, A, B, s);
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-#pragma unroll
-    for (int l = 0; l < 4; ++l) {
-      const int64_t i = i0 + ty * 4 + k, j = j0 + tx * 4 + l;
-      if (i >= c.m || j >= c.d) continue;
-      float* w = c.W + i * c.ldw + j;
-      const double v = (double)c.alpha * s[k][l];
-      *w = (float)(c.accumulate ? (double)*w + v : v);
-    }
-}
-
-int64_t glu_grid(int64_t T, int n) { return cdiv(T, 64) * cdiv(n, 64); }
 int64_t glu_gradients_grid(int64_t T, int f) { return cdiv(T * cdiv(f, 8), 256); }
 
 namespace {
@@ -195,38 +69,94 @@ void with_type(int dtype, F&& go) {
   else go(float{});
 }
 
+ProductCall glu_product(const GluCall& c) {
+  ProductCall p{};
+  p.epi = kEpiGlu;
+  p.act = c.act;
+  p.dtype = c.dtype;
+  p.parts = 1;
+  p.a[0] = {c.wg, c.ldg, c.f, c.d, c.aligned};
+  p.a[1] = {c.wu, c.ldu, c.f, c.d, c.aligned};
+  p.b[0] = {c.x, c.ldx, c.T, c.d, c.aligned};
+  p.M = c.f;
+  p.N = c.T;
+  p.K = c.d;
+  p.out = c.h;
+  p.ldo = c.ldh;
+  p.gate = c.gate;
+  p.up = c.up;
+  p.ldz = c.ldz;
+  p.ldup = c.ldup;
+  p.work = c.work;
+  return p;
+}
+
+ProductCall dx_product(const GluGradCall& c) {
+  ProductCall p{};
+  p.epi = kEpiStore;
+  p.dtype = c.dtype;
+  p.parts = 2;
+  p.a[0] = {c.wg, c.ldg, c.f, c.d, c.aligned};
+  p.a[1] = {c.wu, c.ldu, c.f, c.d, c.aligned};
+  p.b[0] = {c.dgate, c.lddz, c.T, c.f, c.aligned};
+  p.b[1] = {c.dup, c.lddup, c.T, c.f, c.aligned};
+  p.M = c.d;
+  p.N = c.T;
+  p.K = c.f;
+  p.out = c.dx;
+  p.ldo = c.lddx;
+  p.work = c.work;
+  return p;
+}
+
+ProductCall grad_product(const WgradXCall& c) {
+  ProductCall p{};
+  p.epi = kEpiGrad;
+  p.dtype = c.dtype;
+  p.parts = 1;
+  p.a[0] = {c.x, c.ldx, c.T, c.d, c.aligned};
+  p.b[0] = {c.delta, c.ldd, c.T, c.m, c.aligned};
+  p.M = c.d;
+  p.N = c.m;
+  p.K = c.T;
+  p.out = c.W;
+  p.ldo = c.ldw;
+  p.alpha = c.alpha;
+  p.accumulate = c.accumulate;
+  p.work = c.work;
+  return p;
+}
+
 }  // namespace
+
+size_t glu_forward_workspace(const GluCall& c) { return c.T ? product_workspace(glu_product(c)) : 0; }
+size_t glu_backward_workspace(const GluGradCall& c) { return c.T ? product_workspace(dx_product(c)) : 0; }
+size_t wgrad_x_workspace(const WgradXCall& c) { return c.T ? product_workspace(grad_product(c)) : 0; }
 
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s) {
   if (c.T == 0) return hipSuccess;
-  with_type(c.dtype, [&](auto t) {
-    with_act(c.act, [&](auto a) {
-      hipLaunchKernelGGL((k_glu_forward<decltype(t), decltype(a)::value>), dim3((unsigned)glu_grid(c.T, c.f)), dim3(256),
-                         0, s, c, drop);
-    });
-  });
-  return hipGetLastError();
+  return launch_product(glu_product(c), drop, s);
 }
 
 hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s) {
   if (c.T == 0) return hipSuccess;
   with_type(c.dtype, [&](auto t) {
-    using E = decltype(t);
     with_act(c.act, [&](auto a) {
-      hipLaunchKernelGGL((k_glu_gradients<E, decltype(a)::value>), dim3((unsigned)glu_gradients_grid(c.T, c.f)), dim3(256),
-                         0, s, c, drop, (int)cdiv(c.f, 8), c.T * cdiv(c.f, 8));
+      hipLaunchKernelGGL((k_glu_gradients<decltype(t), decltype(a)::value>), dim3((unsigned)glu_gradients_grid(c.T, c.f)),
+                         dim3(256), 0, s, c, drop, (int)cdiv(c.f, 8), c.T * cdiv(c.f, 8));
     });
-    if (c.dx) hipLaunchKernelGGL(k_glu_dx<E>, dim3((unsigned)glu_grid(c.T, c.d)), dim3(256), 0, s, c);
   });
+  if (c.dx) return launch_product(dx_product(c), DropArgs{}, s);
   return hipGetLastError();
 }
 
 hipError_t launch_wgrad_x(const WgradXCall& c, hipStream_t s) {
-  if (c.T == 0 && c.accumulate) return hipSuccess;
-  with_type(c.dtype, [&](auto t) {
-    hipLaunchKernelGGL(k_wgrad_x<decltype(t)>, dim3((unsigned)glu_grid(c.m, c.d)), dim3(256), 0, s, c);
-  });
-  return hipGetLastError();
+  if (c.T == 0) {
+    if (c.accumulate) return hipSuccess;
+    hipLaunchKernelGGL(k_wgrad_none, dim3((unsigned)cdiv((int64_t)c.m * c.d, 256)), dim3(256), 0, s, c.W, c.ldw, c.m, c.d);
+    return hipGetLastError();
+  }
+  return launch_product(grad_product(c), DropArgs{}, s);
 }
 
 }  // namespace gift

@@ -500,7 +500,7 @@ gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, in
  * that was kept whole.  bf16 and fp16 products are exact in the fp32 sums.  An fp32 operand is the sum of three bf16
  * numbers, of whose nine products the six largest are added: what is left out is below 2^-24 of |delta| |x|; an
  * infinity in an fp32 operand gives NaN.  Sums are fp32, in the same order on every call.
- * d_W may not overlap delta or x. */
+ * d_W may not overlap delta or x.  Workspace and `aligned` (of delta and x): see gift_glu_forward. */
 size_t gift_weight_grad_x_workspace_bytes(int64_t T, int32_t m, int32_t d, int32_t dtype, int32_t aligned);
 gift_status gift_weight_grad_x(const void* d_delta, int32_t dtype, int64_t ldd, int32_t m, const void* d_x,
                                int64_t ldx, int64_t T, int32_t d, float alpha, int32_t accumulate, float* d_W,
@@ -537,13 +537,15 @@ gift_status gift_dropout_apply(const gift_dropout* h_drop, const void* d_x, int3
 /* Gated feed-forward block, x [T][d], Wg and Wu [f][d] (halves of one [2 f][d] matrix or separate):
  *   z = x Wg^T, u = x Wu^T, h = D(act(z) u)
  * act(z): silu z s(z), gelu z N(z) (N the normal distribution function), gelu_tanh z s(2 sqrt(2 / pi) (z + 0.044715
- * z^3)), relu max(z, 0), sigmoid s(z), with s(z) = 1 / (1 + e^-z). */
+ * z^3)), relu max(z, 0), sigmoid s(z), with s(z) = 1 / (1 + e^-z).
+ * Products take d, f and m up to 2^21 (GIFT_ERR_UNSUPPORTED beyond). */
 enum gift_act { GIFT_ACT_SILU = 0, GIFT_ACT_GELU = 1, GIFT_ACT_GELU_TANH = 2, GIFT_ACT_RELU = 3, GIFT_ACT_SIGMOID = 4 };
 /* h, from the fp32 sums z and u, is rounded once to `dtype`.  d_gate, d_up [T][f] (both or neither): z and u rounded
  * to `dtype`, for the backward pass.  h_drop: NULL for none.  h_ckpt: h [T][f] as it was rounded is also saved there.
  * Outputs may overlap neither an input nor each other.  fp32 products as in gift_weight_grad_x.
- * d_work: 16-byte aligned, gift_glu_workspace_bytes; `aligned` there is nonzero when
- * d_x, d_wg and d_wu and their rows are 16-byte aligned (else the call first lays them out anew in the workspace). */
+ * d_work: 16-byte aligned, gift_glu_workspace_bytes (0: NULL will do), free to be used again by what follows on the
+ * stream.  `aligned` there is nonzero when d_x, d_wg and d_wu and their rows are 16-byte aligned and rows at most 4 MB
+ * apart; other operands are first laid out anew in the workspace, which takes more of it. */
 size_t gift_glu_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t dtype, int32_t aligned);
 gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_t ldx, int64_t T, int32_t d,
                              const void* d_wg, int64_t ldg, const void* d_wu, int64_t ldu, int32_t f,
@@ -556,7 +558,7 @@ gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_
  * the weight gradients (gift_weight_grad, gift_weight_grad_x) too.  d_dx NULL: dgate and dup only (the weights and
  * the workspace are not used).  dgate and dup may each be dh, gate or up, with the same leading dimension; any other
  * overlap with them, of each other, or of dx with dgate, dup or the weights is refused.
- * `aligned`: of dgate, dup, Wg and Wu. */
+ * `aligned`: as above, of dgate, dup, Wg and Wu, when besides lddz == lddup and ldg == ldu. */
 size_t gift_glu_backward_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t dtype, int32_t aligned);
 gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int64_t lddh, int64_t T, int32_t f,
                               const void* d_gate, int64_t ldz, const void* d_up, int64_t ldup,
