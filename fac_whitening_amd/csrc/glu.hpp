@@ -63,6 +63,10 @@ __device__ __forceinline__ float act_value(float z, float* grad = nullptr) {
     if (grad) *grad = z > 0.f ? 1.f : z == z ? 0.f : z;
     return z > 0.f ? z : z == z ? 0.f : z;
   } else if constexpr (ACT == GIFT_ACT_SILU || ACT == GIFT_ACT_SIGMOID) {
+    if (!grad) {   // (e^-z is infinite, s(z) zero, where it is below 2^-128)
+      const float s = reciprocal(1.f + exp_neg(z));
+      return ACT == GIFT_ACT_SIGMOID ? s : z * s;
+    }
     const float e = exp_neg(__builtin_fabsf(z)), r = reciprocal(1.f + e);
     const float s = z >= 0.f ? r : e * r, q = z >= 0.f ? e * r : r;   // s(z) and s(-z)
     if constexpr (ACT == GIFT_ACT_SIGMOID) {

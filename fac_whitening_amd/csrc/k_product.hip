@@ -91,7 +91,8 @@ struct PTile {
   static constexpr int KT = 64;                                // elements of the long axis a stage
   static constexpr int SA = 64 * MT, SB = 64 * NT;             // rows of a tile's operands
   static constexpr int kBytesA = SA * 128, kBytesB = SB * 128, kStage = kBytesA + kBytesB;
-  static constexpr int kLds = 2 * kStage + 16384;
+  static constexpr int kTurn = 4096;                           // a wave's LDS for outputs
+  static constexpr int kLds = 2 * kStage + 4 * kTurn;
   static constexpr int LA = kBytesA / 4096, LB = kBytesB / 4096;   // direct loads of a wave a stage
   static constexpr int KS = 4, PS = MT * NT;                   // steps of 16; products of a step
 };
@@ -127,10 +128,10 @@ __device__ __forceinline__ void pack4(const float* v, uint32_t* w) {
 
 // 16 bytes of elements to p, n of them valid.
 template <typename TO>
-__device__ __forceinline__ void store16(TO* p, const uint32_t* w, int n) {
+__device__ __forceinline__ void store16(TO* p, const uint32_t* w, int n, bool stream) {
   constexpr int N = OutVec<TO>::N;
   if (n >= N) {
-    store_words<4>(p, w, false);
+    store_words<4>(p, w, stream);
   } else {
 #pragma unroll
     for (int i = 0; i < N - 1; ++i)
@@ -468,100 +469,123 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
           }
       continue;
     }
-    // Each wave turns 32 outputs x 32 (or 64 of 16 bits) into rows in its own 4 KB of LDS.
+    // Each wave turns 32 outputs x 32 (or 64 of 16 bits) into rows in its own 4 KB of LDS.  Its LDS operations run
+    // in order, so a block's rows are read back while the next block is computed and written over them.
     constexpr int XO = GLU ? MT / 2 : MT;                            // 32-wide output tiles along i
     constexpr int XB = sizeof(TO) == 2 && XO >= 2 ? 2 : 1;           // of which this many at a time
     constexpr int CH = XB * 32 / OutVec<TO>::N;                      // 16-byte chunks of a row
-    char* mine = lds + 2 * C::kStage + wave * 4096;
+    constexpr int kRows = CH / 2;
+    char* mine = lds + 2 * C::kStage + wave * C::kTurn;
     const int i0 = ti * (GLU ? C::SA / 2 : C::SA) + wm * 32 * XO;
     const int64_t j0 = (int64_t)tj * C::SB + wn * 32 * NT;
+    const bool stream = o.stream != 0;
     DropArgs drop{};
     if constexpr (GLU) drop = drop_args_of(o);
     const uint64_t offset = GLU && drop.on ? drop_offset(drop) : 0;
+    // block b of three (z, u and h) or one for each place, places along i first
+    auto fill = [&](auto BC, auto WC) {
+      constexpr int b = decltype(BC)::value, of = decltype(WC)::value, what = of == 3 ? b % 3 : 2;
+      constexpr int xb = b / of % (XO / XB) * XB, y = b / of / (XO / XB);
+      char* to = mine;
 #pragma unroll
-    for (int y = 0; y < NT; ++y) {
+      for (int q = 0; q < XB; ++q) {
+        uint32_t bits[4][2];
+        if (GLU && what == 2 && drop.on) {
+          // the lanes of the lower half draw for columns 0 .. 15 of the 32, those of the upper for 16 .. 31; of each
+          // eight columns the lower half then takes the first four
 #pragma unroll
-      for (int xb = 0; xb < XO; xb += XB) {
-        unrolled<0, GLU ? 3 : 1>([&](auto WC) {
-          constexpr int what = GLU ? decltype(WC)::value : 2;        // z, u, the output
-          if (what < 2 && !o.gate) return;
-          asm volatile("" : "+v"(el));
+          for (int n = 0; n < 2; ++n) {
+            uint32_t w[4];
+            drop_bits(drop, offset, (uint32_t)(j0 + 32 * y + (el & 31)), (uint32_t)(i0 + 32 * (xb + q)) / 8 + 2 * (el >> 5) + n,
+                      w);
+            const auto p0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+            const auto p1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+            bits[n][0] = p0[0];
+            bits[n][1] = p1[0];
+            bits[n + 2][0] = p0[1];
+            bits[n + 2][1] = p1[1];
+          }
+        }
 #pragma unroll
-          for (int q = 0; q < XB; ++q) {
-            uint32_t bits[4][2];
-            if (GLU && what == 2 && drop.on) {
-              // the lanes of the lower half draw for columns 0 .. 15 of the 32, those of the upper for 16 .. 31; of each
-              // eight columns the lower half then takes the first four
+        for (int e = 0; e < 4; ++e) {
+          float v[4];
+          if constexpr (GLU) {
+            hold(acc[2 * (xb + q)][y]);
+            hold(acc[2 * (xb + q) + 1][y]);
+          } else {
+            hold(acc[xb + q][y]);
+          }
 #pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                uint32_t w[4];
-                drop_bits(drop, offset, (uint32_t)(j0 + 32 * y + (el & 31)),
-                          (uint32_t)(i0 + 32 * (xb + q)) / 8 + 2 * (el >> 5) + n, w);
-                const auto p0 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-                const auto p1 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-                bits[n][0] = p0[0];
-                bits[n][1] = p1[0];
-                bits[n + 2][0] = p0[1];
-                bits[n + 2][1] = p1[1];
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float v[4];
-              if constexpr (GLU) {
-                hold(acc[2 * (xb + q)][y]);
-                hold(acc[2 * (xb + q) + 1][y]);
-              } else {
-                hold(acc[xb + q][y]);
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if constexpr (GLU) {
-                  const float z = acc[2 * (xb + q)][y][4 * e + i], u = acc[2 * (xb + q) + 1][y][4 * e + i];
-                  v[i] = what == 0 ? z : what == 1 ? u : act_value<ACT>(z) * u;
-                  if (what == 2 && drop.on) v[i] = drop_one(drop, bits[e], i, v[i]);
-                } else {
-                  v[i] = acc[xb + q][y][4 * e + i];
-                  if constexpr (EPI == kEpiGrad) v[i] *= o.alpha;
-                }
-              }
-              uint32_t w[4];
-              pack4<TO>(v, w);
-              const int t = el & 31, hi = el >> 5;
-              if constexpr (sizeof(TO) == 2) {
-                const pu32x2 p = {w[0], w[1]};
-                *reinterpret_cast<pu32x2*>(mine + t * (CH * 16) + (((4 * q + e) ^ (t & (CH - 1))) * 16 + hi * 8)) = p;
-              } else {
-                const pu32x4 p = {w[0], w[1], w[2], w[3]};
-                *reinterpret_cast<pu32x4*>(mine + t * (CH * 16) + ((2 * e + hi) ^ (t & (CH - 1))) * 16) = p;
-              }
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (GLU) {
+              const float z = acc[2 * (xb + q)][y][4 * e + i], u = acc[2 * (xb + q) + 1][y][4 * e + i];
+              v[i] = what == 0 ? z : what == 1 ? u : act_value<ACT>(z) * u;
+              if (what == 2 && drop.on) v[i] = drop_one(drop, bits[e], i, v[i]);
+            } else {
+              v[i] = acc[xb + q][y][4 * e + i];
+              if constexpr (EPI == kEpiGrad) v[i] *= o.alpha;
             }
           }
-          __builtin_amdgcn_wave_barrier();
-          TO* out = static_cast<TO*>(what == 0 ? o.gate : what == 1 ? o.up : o.out);
-          const int64_t ld = what == 0 ? o.ldz : what == 1 ? o.ldup : o.ldo;
-          const int col = i0 + 32 * xb + (el % CH) * OutVec<TO>::N;
-#pragma unroll
-          for (int r = 0; r < CH / 2; ++r) {
-            const int row = r * (64 / CH) + el / CH;
-            const pu32x4 v = *reinterpret_cast<const pu32x4*>(mine + row * (CH * 16) + ((el % CH) ^ (row & (CH - 1))) * 16);
-            const int64_t t = j0 + 32 * y + row;
-            if (t < a.N && col < a.M) {
-              uint32_t w[4] = {v[0], v[1], v[2], v[3]};
-              TO* p = out + t * ld + col;
-              if (EPI == kEpiGrad && o.accumulate) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (col + i < a.M) w[i] = __float_as_uint(__uint_as_float(w[i]) + reinterpret_cast<const float*>(p)[i]);
-              }
-              store16<TO>(p, w, a.M - col);
-            }
+          uint32_t w[4];
+          pack4<TO>(v, w);
+          const int t = el & 31, hi = el >> 5;
+          if constexpr (sizeof(TO) == 2) {
+            const pu32x2 p = {w[0], w[1]};
+            *reinterpret_cast<pu32x2*>(to + t * (CH * 16) + (((4 * q + e) ^ (t & (CH - 1))) * 16 + hi * 8)) = p;
+          } else {
+            const pu32x4 p = {w[0], w[1], w[2], w[3]};
+            *reinterpret_cast<pu32x4*>(to + t * (CH * 16) + ((2 * e + hi) ^ (t & (CH - 1))) * 16) = p;
           }
-          __builtin_amdgcn_wave_barrier();
-          __builtin_amdgcn_sched_barrier(0);
-        });
+        }
       }
-    }
+      __builtin_amdgcn_wave_barrier();
+    };
+    pu32x4 out[kRows];
+    auto fetch = [&]() {
+      const char* from = mine;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int row = r * (64 / CH) + el / CH;
+        out[r] = *reinterpret_cast<const pu32x4*>(from + row * (CH * 16) + ((el % CH) ^ (row & (CH - 1))) * 16);
+      }
+    };
+    auto write = [&](auto BC, auto WC) {
+      constexpr int b = decltype(BC)::value, of = decltype(WC)::value, what = of == 3 ? b % 3 : 2;
+      constexpr int xb = b / of % (XO / XB) * XB, y = b / of / (XO / XB);
+      TO* to = static_cast<TO*>(what == 0 ? o.gate : what == 1 ? o.up : o.out);
+      const int64_t ld = what == 0 ? o.ldz : what == 1 ? o.ldup : o.ldo;
+      asm volatile("" : "+v"(el));
+      const int col = i0 + 32 * xb + (el % CH) * OutVec<TO>::N;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int64_t t = j0 + 32 * y + r * (64 / CH) + el / CH;
+        if (t < a.N && col < a.M) {
+          uint32_t w[4] = {out[r][0], out[r][1], out[r][2], out[r][3]};
+          TO* p = to + t * ld + col;
+          if (EPI == kEpiGrad && o.accumulate) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (col + i < a.M) w[i] = __float_as_uint(__uint_as_float(w[i]) + reinterpret_cast<const float*>(p)[i]);
+          }
+          store16<TO>(p, w, a.M - col, stream);
+        }
+      }
+    };
+    auto blocks = [&](auto WC) {
+      constexpr int n = NT * (XO / XB) * decltype(WC)::value;
+      fill(std::integral_constant<int, 0>{}, WC);
+      unrolled<0, n>([&](auto BC) {
+        constexpr int b = decltype(BC)::value;
+        fetch();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (b + 1 < n) fill(std::integral_constant<int, b + 1>{}, WC);
+        __builtin_amdgcn_sched_barrier(0);
+        write(BC, WC);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    if (GLU && o.gate) blocks(std::integral_constant<int, GLU ? 3 : 1>{});
+    else blocks(std::integral_constant<int, 1>{});
   }
   wait_vm<0>();   // loads into LDS have to end before the workgroup does
 }
@@ -861,6 +885,7 @@ hipError_t launch_product(const ProductCall& c, const DropArgs& drop, hipStream_
   o.drop = drop;
   o.alpha = c.alpha;
   o.accumulate = c.accumulate;
+  o.stream = c.N * c.M * (c.dtype == GIFT_FP32 || c.epi == kEpiGrad ? 4 : 2) > kStreamBytes;
   if (c.dtype == GIFT_BF16) product_types<Bf16, Bf16>(c, a, o, p, s);
   else if (c.dtype == GIFT_FP16) product_types<Fp16, Fp16>(c, a, o, p, s);
   else product_types<Bf16, float>(c, a, o, p, s);

@@ -92,6 +92,7 @@ struct ProdOut {
   DropArgs drop;
   float alpha;
   int accumulate;
+  int stream;           // outputs larger than the caches are written past them
 };
 
 // One operand in the caller's memory, [rows][cols]; rows == 0: none.
