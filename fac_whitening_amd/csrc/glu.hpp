@@ -57,18 +57,21 @@ __device__ __forceinline__ float drop_one(const DropArgs& a, const uint32_t* w, 
 __device__ __forceinline__ float exp_neg(float v) { return __builtin_amdgcn_exp2f(v * -1.4426950408889634f); }
 __device__ __forceinline__ float reciprocal(float v) { return __builtin_amdgcn_rcpf(v); }
 
+// s(v) = 1 / (1 + e^-v), and s(-v).  (e^-v is infinite, and s zero, where s is below 2^-128.)
+__device__ __forceinline__ float logistic(float v, float* other) {
+  const float e = exp_neg(v), s = reciprocal(1.f + e);
+  *other = v >= 0.f ? e * s : 1.f - s;
+  return s;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z, float* grad = nullptr) {
   if constexpr (ACT == GIFT_ACT_RELU) {
     if (grad) *grad = z > 0.f ? 1.f : z == z ? 0.f : z;
     return z > 0.f ? z : z == z ? 0.f : z;
   } else if constexpr (ACT == GIFT_ACT_SILU || ACT == GIFT_ACT_SIGMOID) {
-    if (!grad) {   // (e^-z is infinite, s(z) zero, where it is below 2^-128)
-      const float s = reciprocal(1.f + exp_neg(z));
-      return ACT == GIFT_ACT_SIGMOID ? s : z * s;
-    }
-    const float e = exp_neg(__builtin_fabsf(z)), r = reciprocal(1.f + e);
-    const float s = z >= 0.f ? r : e * r, q = z >= 0.f ? e * r : r;   // s(z) and s(-z)
+    float q;
+    const float s = logistic(z, &q);
     if constexpr (ACT == GIFT_ACT_SIGMOID) {
       if (grad) *grad = s * q;
       return s;
@@ -95,8 +98,8 @@ __device__ __forceinline__ float act_value(float z, float* grad = nullptr) {
   } else {
     constexpr float k = 1.5957691216057308f;   // 2 sqrt(2 / pi)
     const float w = k * (z + 0.044715f * z * z * z);
-    const float e = exp_neg(__builtin_fabsf(w)), r = reciprocal(1.f + e);
-    const float s = w >= 0.f ? r : e * r, q = w >= 0.f ? e * r : r;
+    float q;
+    const float s = logistic(w, &q);
     if (grad) *grad = s + z * (s * q) * (k * (1.f + 0.134145f * z * z));
     return z * s;
   }
