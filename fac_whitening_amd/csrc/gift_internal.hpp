@@ -344,6 +344,13 @@ int64_t glu_gradients_grid(int64_t T, int f);
 size_t glu_forward_workspace(const GluCall& c);
 size_t glu_backward_workspace(const GluGradCall& c);
 size_t wgrad_x_workspace(const WgradXCall& c);
+// Whether k_glu_tokens makes the block's output: up to 32 rows of x, and up to 64 where the weights are small (tokens
+// against tiles, 64 rows bf16: 1536 x 6144 22 and 30 us, 4096 x 16384 111 and 85; three fp32 planes of 64 rows do not fit
+// its registers).
+inline bool glu_by_tokens(int dtype, int64_t T, int d, int f) {
+  return T <= 32 || (T <= 64 && dtype != GIFT_FP32 && (int64_t)d * f <= (int64_t)1 << 24);
+}
+hipError_t launch_glu_tokens(const GluCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_wgrad_x(const WgradXCall& c, hipStream_t s);

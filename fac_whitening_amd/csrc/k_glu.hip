@@ -129,13 +129,13 @@ ProductCall grad_product(const WgradXCall& c) {
 
 }  // namespace
 
-size_t glu_forward_workspace(const GluCall& c) { return c.T ? product_workspace(glu_product(c)) : 0; }
+size_t glu_forward_workspace(const GluCall& c) { return glu_by_tokens(c.dtype, c.T, c.d, c.f) ? 0 : product_workspace(glu_product(c)); }
 size_t glu_backward_workspace(const GluGradCall& c) { return c.T ? product_workspace(dx_product(c)) : 0; }
 size_t wgrad_x_workspace(const WgradXCall& c) { return c.T ? product_workspace(grad_product(c)) : 0; }
 
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s) {
   if (c.T == 0) return hipSuccess;
-  return launch_product(glu_product(c), drop, s);
+  return glu_by_tokens(c.dtype, c.T, c.d, c.f) ? launch_glu_tokens(c, drop, s) : launch_product(glu_product(c), drop, s);
 }
 
 hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s) {

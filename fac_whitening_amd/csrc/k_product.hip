@@ -86,13 +86,13 @@ __device__ __forceinline__ uint64_t uni64(uint64_t v) {
   return (uint64_t)(uint32_t)uni((int)(uint32_t)v) | (uint64_t)(uint32_t)uni((int)(uint32_t)(v >> 32)) << 32;
 }
 
-template <int MT, int NT>
+template <int MT, int NT, int NBUF>
 struct PTile {
   static constexpr int KT = 64;                                // elements of the long axis a stage
   static constexpr int SA = 64 * MT, SB = 64 * NT;             // rows of a tile's operands
   static constexpr int kBytesA = SA * 128, kBytesB = SB * 128, kStage = kBytesA + kBytesB;
   static constexpr int kTurn = 4096;                           // a wave's LDS for outputs
-  static constexpr int kLds = 2 * kStage + 4 * kTurn;
+  static constexpr int kLds = NBUF * kStage + 4 * kTurn;
   static constexpr int LA = kBytesA / 4096, LB = kBytesB / 4096;   // direct loads of a wave a stage
   static constexpr int KS = 4, PS = MT * NT;                   // steps of 16; products of a step
 };
@@ -147,10 +147,10 @@ __device__ __forceinline__ void store16(TO* p, const uint32_t* w, int n, bool st
 }
 
 // Products, E: operand type, TO: output type.
-template <typename E, typename TO, int EPI, int ACT, int MT, int NT, bool AX, bool BX, int WGS>
+template <typename E, typename TO, int EPI, int ACT, int MT, int NT, bool AX, bool BX, int NBUF, int WGS>
 __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
   const auto* const ka = &args.a;
-  using C = PTile<MT, NT>;
+  using C = PTile<MT, NT, NBUF>;
   using Fr = Frag8<E>;
   constexpr bool GLU = EPI == kEpiGlu;
   constexpr int kLoadsA = AX ? 0 : C::LA, kLoadsB = BX ? 0 : C::LB;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
         lj = uni(tj);
         const int s0 = uni(w.s0);
         real = uni(w.s1) - s0;
-        left = (real + 1) & ~1;          // stages come in pairs; the last may be empty
+        left = X ? (real + 1) & ~1 : real;   // (transposing: stages come in pairs; the last may be empty)
         lseg = uni(s0 / nst);
         lk = s0 - lseg * nst;
         fresh = true;
@@ -290,13 +290,13 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
   };
   auto direct = [&](const Desc& D, int base, int q) {
     if (q < kLoadsA) {
-      const uint32_t at = lds0 + base + (4 * q + wave) * 1024;
+      const uint32_t to = lds0 + base + (4 * q + wave) * 1024;
       if constexpr (GLU) {
         // row blocks of gate and up in turn: block q is rows 32 (q / 2) of one of them
         const int off = (q & 1 ? offu : offa) + (q & 1 ? odd : 0);
-        dma16(q & 1 ? D.u : D.a, at, row_off(off, (uint32_t)((q >> 1) * 32) * (q & 1 ? ldu2 : lda2)) | D.mask[q & 1]);
+        dma16(q & 1 ? D.u : D.a, to, row_off(off, (uint32_t)((q >> 1) * 32) * (q & 1 ? ldu2 : lda2)) | D.mask[q & 1]);
       } else {
-        dma16(D.a, at, place(offa, q, lda2, D));
+        dma16(D.a, to, place(offa, q, lda2, D));
       }
     } else {
       const int p = q - kLoadsA;
@@ -349,34 +349,43 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
   };
   pf32x16 acc[MT][NT];
 
-  // ---- prologue: stages 0 and 1 (transposing: 2 in registers) ----
+  // ---- prologue ----
   Desc D2;
-  {
-    const Desc D0 = next_stage();
+  if constexpr (!X) {
+    static_assert((NBUF - 1) * (kLoadsA + kLoadsB) < 64, "vmcnt");
 #pragma unroll
-    for (int q = 0; q < kLoadsA + kLoadsB; ++q) direct(D0, 0, q);
+    for (int st = 0; st < NBUF; ++st) {
+      D2 = next_stage();
+#pragma unroll
+      for (int q = 0; q < kLoadsA + kLoadsB; ++q) direct(D2, st * C::kStage, q);
+    }
+    wait_vm<(NBUF - 1) * (kLoadsA + kLoadsB)>();
+    bare_barrier();
+  } else {
+    static_assert(NBUF == 2, "transposing sides have two buffers");
     auto load_all = [&](Raw& x, const Desc& D) {
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int r = 0; r < 8; ++r) load_x(x, D, n, r);
     };
-    if constexpr (X) load_all(raw[0], D0);
+    const Desc D0 = next_stage();
+#pragma unroll
+    for (int q = 0; q < kLoadsA + kLoadsB; ++q) direct(D0, 0, q);
+    load_all(raw[0], D0);
     const Desc D1 = next_stage();
 #pragma unroll
     for (int q = 0; q < kLoadsA + kLoadsB; ++q) direct(D1, C::kStage, q);
-    if constexpr (X) {
-      load_all(raw[1], D1);
+    load_all(raw[1], D1);
 #pragma unroll
-      for (int n = 0; n < NS; ++n)
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          turn(raw[0], n, c);
-          put(n, c, 0);
-        }
-      D2 = next_stage();
-      load_all(raw[0], D2);
-    }
+      for (int c = 0; c < 8; ++c) {
+        turn(raw[0], n, c);
+        put(n, c, 0);
+      }
+    D2 = next_stage();
+    load_all(raw[0], D2);
     wait_lds();
     wait_vm<0>();
     bare_barrier();
@@ -384,12 +393,11 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
 #pragma unroll
   for (int k = 0; k < NT + MT; ++k) read(F[0], 0, 0, k);
 
-  // Stage s in the buffer at BASE: its products; transposing sides turn stage
-  // s + 1 (registers `x`) into the other buffer and load stage s + 3; behind the
-  // barrier, which every wave reaches with its last operands read, direct
-  // sides load stage s + 2 into this buffer.
-  auto stage = [&](Raw& x, auto BASE) {
-    constexpr int base = decltype(BASE)::value, nbase = C::kStage - base;
+  // Stage s in the buffer at `base`, the next one at `nbase`: its products.  Transposing sides turn stage s + 1
+  // (registers `x`) into the other buffer and load stage s + 3.  Behind the barrier, which every wave reaches with its
+  // last operands read, direct sides load stage s + NBUF into this buffer.
+  auto stage = [&](Raw& x, auto BASE, auto NBASE) {
+    const int base = BASE, nbase = NBASE;
     constexpr int kBefore = 3 * C::PS;                            // products in front of the barrier
     // items in front of the barrier, 24 a block: turned (a step and a write a column), then loaded
     constexpr int kItems = 24 * NS;
@@ -399,7 +407,7 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
       constexpr int ks = decltype(KSC)::value;
       if constexpr (ks == 3) {
         wait_lds();
-        if constexpr (!X) wait_vm<0>();
+        if constexpr (!X) wait_vm<(NBUF - 2) * (kLoadsA + kLoadsB)>();   // (later stages may be in flight)
         else if constexpr (kLoadsA + kLoadsB > 0) wait_vm<8>();   // (this stage's 8 loads into registers may be in flight)
         bare_barrier();
         if constexpr (!X) D2 = next_stage();
@@ -426,6 +434,7 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
     if constexpr (X) D2 = D3;
   };
 
+  int at = 0;   // the buffer of the next stage
   Piece w;
   for (int piece = 0; product_piece(&kernel_args()->a, g, piece, w); ++piece) {
     int ti, tj;
@@ -439,9 +448,17 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
       for (int y = 0; y < NT; ++y)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.f;
-    for (int st = s0; st < s1; st += 2) {
-      stage(raw[X ? 1 : 0], std::integral_constant<int, 0>{});
-      stage(raw[0], std::integral_constant<int, C::kStage>{});
+    if constexpr (X) {
+      for (int st = s0; st < s1; st += 2) {
+        stage(raw[X ? 1 : 0], std::integral_constant<int, 0>{}, std::integral_constant<int, C::kStage>{});
+        stage(raw[0], std::integral_constant<int, C::kStage>{}, std::integral_constant<int, 0>{});
+      }
+    } else {
+      for (int st = s0; st < s1; ++st) {
+        const int next = at == (NBUF - 1) * C::kStage ? 0 : at + C::kStage;
+        stage(raw[0], at, next);
+        at = next;
+      }
     }
     const auto* const q = kernel_args();
     ConstArgs& a = q->a;
@@ -475,7 +492,7 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
     constexpr int XB = sizeof(TO) == 2 && XO >= 2 ? 2 : 1;           // of which this many at a time
     constexpr int CH = XB * 32 / OutVec<TO>::N;                      // 16-byte chunks of a row
     constexpr int kRows = CH / 2;
-    char* mine = lds + 2 * C::kStage + wave * C::kTurn;
+    char* mine = lds + NBUF * C::kStage + wave * C::kTurn;
     const int i0 = ti * (GLU ? C::SA / 2 : C::SA) + wm * 32 * XO;
     const int64_t j0 = (int64_t)tj * C::SB + wn * 32 * NT;
     const bool stream = o.stream != 0;
@@ -678,9 +695,7 @@ __global__ void __launch_bounds__(256) k_product_join(ProdArgs a, ProdOut o, int
 }
 
 // An operand laid out anew: rows 16-byte aligned, padded with zeros to a
-// multiple of 8 columns; an fp32 operand as three bf16 numbers whose sum it is,
-// each the nearest to what the ones before it leave (the first one truncated
-// where rounding would overflow).
+// multiple of 8 columns; an fp32 operand as three bf16 planes (split_planes).
 template <typename T>
 __global__ void __launch_bounds__(256) k_product_pack(const T* src, int64_t ld, int64_t rows, int cols, uint16_t* dst,
                                                       int64_t ldp, int nb) {
@@ -695,22 +710,7 @@ __global__ void __launch_bounds__(256) k_product_pack(const T* src, int64_t ld, 
   } else {
     float v[8];
     unpack8(x, v);
-#pragma unroll
-    for (int pl = 0; pl < 3; ++pl) {
-      Raw8<Bf16> o;
-      pack8(v, o);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t h = (o.w[i / 2] >> (16 * (i & 1))) << 16;
-        if (pl == 0 && (h & 0x7F800000u) == 0x7F800000u && __builtin_isfinite(v[i])) {
-          h = __float_as_uint(v[i]) & 0xFFFF0000u;
-          o.w[i / 2] = i & 1 ? (o.w[i / 2] & 0xFFFFu) | h : (o.w[i / 2] & 0xFFFF0000u) | h >> 16;
-        }
-        const float rest = v[i] - __uint_as_float(h);
-        v[i] = __builtin_isfinite(v[i]) ? rest : 0.f;
-      }
-      store_words<4>(p + (int64_t)pl * rows * ldp, o.w, false);
-    }
+    split_planes(v, [&](int pl, const uint32_t* w) { store_words<4>(p + (int64_t)pl * rows * ldp, w, false); });
   }
 }
 
@@ -719,19 +719,27 @@ namespace {
 constexpr int kProductGroups = 256;   // compute units of an MI355X
 
 struct ProdPlan {
-  int side, nbm, nbn, nst, unit, grid;
+  int side, deep, nbm, nbn, nst, unit, grid;   // deep: four stages in LDS, one workgroup a compute unit
   int first, split;    // first split tile, split tiles
   size_t bytes;        // of the pieces
 };
 
-// A plan with tiles of `side`, split at multiples of `unit` stages (0: not
-// split), and what it is expected to take, in us.
-double product_try(ProdPlan& p, int side, int unit, int epi, bool ax, bool bx, int64_t M, int64_t N, int64_t K, int nseg) {
+// A plan in one of three forms (tiles of 256, of 128 with two workgroups a
+// compute unit, of 128 with one and four stages in LDS), split at multiples of
+// `unit` stages (0: not split), and what it is expected to take, in us.
+// Measured on bf16 (direct x direct, transposing x direct, both transposing; 1536
+// x 6144 and 4096 x 4096, 128 to 8192 tokens), within a fifth or so:
+//   a stage of a workgroup   256: 1.75 each; 128: 1.0, 1.25, 1.15; deep: 0.6
+//   a whole tile written     256: 6, fp32 gradients 14; 128: 2, 4
+//   a piece written          256: 10, 128: 6
+//   the join                 5 with its launch, pieces at 8 TB/s, outputs at 6
+double product_try(ProdPlan& p, int side, int deep, int unit, int epi, bool ax, bool bx, int64_t M, int64_t N, int64_t K, int nseg) {
   p.side = side;
+  p.deep = deep;
   p.nbm = (int)cdiv(M, epi == kEpiGlu ? side / 2 : side);
   p.nbn = (int)cdiv(N, side);
   p.nst = (int)cdiv(K, 64);
-  p.grid = side == 128 ? 2 * kProductGroups : kProductGroups;
+  p.grid = side == 128 && !deep ? 2 * kProductGroups : kProductGroups;
   const int total = p.nst * nseg;
   p.unit = unit ? unit : total;
   const WLevel v = wgrad_levels(p.nbm * p.nbn, (int)cdiv(total, p.unit), p.grid);
@@ -740,39 +748,49 @@ double product_try(ProdPlan& p, int side, int unit, int epi, bool ax, bool bx, i
   p.split = w.tiles;
   p.bytes = (size_t)w.pieces * side * side * 4;
   const double stages = (double)v.C * p.unit;
-  const bool alone = (int64_t)p.nbm * p.nbn * cdiv(total, p.unit) <= (int64_t)kProductGroups * v.C;
-  const double stage = side == 256 ? 1.75 : alone ? 0.75 : 1.0;
-  const double whole = (stages / total) * (side == 256 ? 6.0 : 2.0);
-  return stages * stage + whole + (p.split ? 5.0 + 2.0 * (double)p.bytes / 4.5e6 : 0.0);
+  const bool large = side == 256, grad = epi == kEpiGrad;
+  const double stage = large ? 1.75 : deep ? 0.6 : bx ? 1.15 : ax ? 1.25 : 1.0;
+  const double whole = (double)(v.C * (int64_t)p.unit / total) * (large ? grad ? 14.0 : 6.0 : grad ? 4.0 : 2.0);
+  const double join = (large ? 10.0 : 6.0) + 5.0 + (double)p.bytes / 8e6 +
+                      (double)p.split * side * side * (grad ? 4 : 2) / 6e6;
+  return stages * stage + whole + (p.split ? join : 0.0);
 }
 
 ProdPlan product_plan(int epi, bool ax, bool bx, int64_t M, int64_t N, int64_t K, int nseg) {
   ProdPlan best{};
   double least = 0;
   if (K < 1) return best;
-  for (int side = 128; side <= 256; side += 128)
+  for (int form = 0; form < 3; ++form) {   // 256, 128, 128 deep
+    if (form == 2 && (ax || bx)) continue;
     for (int unit = 0; unit <= 8; unit += unit ? unit : 2) {
       ProdPlan p{};
-      const double t = product_try(p, side, unit, epi, ax, bx, M, N, K, nseg);
+      const double t = product_try(p, form == 0 ? 256 : 128, form == 2, unit, epi, ax, bx, M, N, K, nseg);
       if (best.side == 0 || t < least) {
         best = p;
         least = t;
       }
     }
+  }
   return best;
 }
 
 template <typename E, typename TO, int EPI, int ACT, bool AX, bool BX>
 void product_go(const ProdArgs& a, const ProdOut& o, const ProdPlan& p, hipStream_t s) {
   if (p.side == 256) {
-    hipLaunchKernelGGL((k_product<E, TO, EPI, ACT, 4, 4, AX, BX, 1>), dim3((unsigned)p.grid), dim3(256), 0, s,
+    hipLaunchKernelGGL((k_product<E, TO, EPI, ACT, 4, 4, AX, BX, 2, 1>), dim3((unsigned)p.grid), dim3(256), 0, s,
                        KernelArgs{a, o});
     if (p.split)
       hipLaunchKernelGGL((k_product_join<TO, EPI, ACT, 4, 4>), dim3((unsigned)(p.split * 16)), dim3(256), 0, s, a, o,
                          p.grid, p.first);
   } else {
-    hipLaunchKernelGGL((k_product<E, TO, EPI, ACT, 2, 2, AX, BX, 2>), dim3((unsigned)p.grid), dim3(256), 0, s,
-                       KernelArgs{a, o});
+    if constexpr (!AX && !BX) {
+      if (p.deep)
+        hipLaunchKernelGGL((k_product<E, TO, EPI, ACT, 2, 2, AX, BX, 4, 1>), dim3((unsigned)p.grid), dim3(256), 0, s,
+                           KernelArgs{a, o});
+    }
+    if (!p.deep)
+      hipLaunchKernelGGL((k_product<E, TO, EPI, ACT, 2, 2, AX, BX, 2, 2>), dim3((unsigned)p.grid), dim3(256), 0, s,
+                         KernelArgs{a, o});
     if (p.split)
       hipLaunchKernelGGL((k_product_join<TO, EPI, ACT, 2, 2>), dim3((unsigned)(p.split * 8)), dim3(256), 0, s, a, o, p.grid,
                          p.first);

@@ -26,6 +26,26 @@ __device__ __forceinline__ pf32x16 mfma32(const pf16x8& a, const pf16x8& b, cons
 template <typename E>
 using Frag8 = std::conditional_t<std::is_same<E, Fp16>::value, pf16x8, pbf16x8>;
 
+// Three bf16 numbers whose sum is v, each the nearest to what the ones before
+// it leave: put(plane, four words of eight values).  (The first is at most the
+// largest bf16 number, which values beyond it would round past; of an infinity
+// or NaN at least one is not finite.)
+template <typename F>
+__device__ __forceinline__ void split_planes(float* v, F&& put) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = p == 0 ? __builtin_amdgcn_fmed3f(v[i], -0x1.FEp127f, 0x1.FEp127f) : v[i];
+    Raw8<Bf16> o;
+    pack8(r, o);
+    unpack8(o, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] -= r[i];
+    put(p, o.w);
+  }
+}
+
 // f(integral_constant<int, B>) ... f(integral_constant<int, E - 1>)
 template <int B, int E, typename F>
 __device__ __forceinline__ void unrolled(F&& f) {
