@@ -319,7 +319,8 @@ struct GluGradCall {
   int64_t ldg, ldu;
   void* dx;
   int64_t lddx;
-  bool aligned;         // rows of dgate, dup and the weights; both of each the same distance apart
+  bool aligned;         // rows of dgate and dup (see ProdOperand), both the same distance apart
+  bool near;            // rows of the weights, both the same distance apart
   void* work;
 };
 struct WgradXCall {
@@ -334,7 +335,7 @@ struct WgradXCall {
   int accumulate;
   float* W;
   int64_t ldw;
-  bool aligned;         // rows of delta and x
+  bool near;            // rows of delta and x (see ProdOperand)
   void* work;
 };
 int64_t dropout_grid(int64_t T, int d);
@@ -345,10 +346,10 @@ size_t glu_forward_workspace(const GluCall& c);
 size_t glu_backward_workspace(const GluGradCall& c);
 size_t wgrad_x_workspace(const WgradXCall& c);
 // Whether k_glu_tokens makes the block's output: up to 32 rows of x, and up to 64 where the weights are small (tokens
-// against tiles, 64 rows bf16: 1536 x 6144 22 and 30 us, 4096 x 16384 111 and 85; three fp32 planes of 64 rows do not fit
-// its registers).
+// against tiles, 64 rows bf16: 1536 x 6144 22 and 23 us, 4096 x 16384 111 and 68) or fp32, whose tiles need their
+// operands laid out anew (1536 x 6144: 64 and 88).
 inline bool glu_by_tokens(int dtype, int64_t T, int d, int f) {
-  return T <= 32 || (T <= 64 && dtype != GIFT_FP32 && (int64_t)d * f <= (int64_t)1 << 24);
+  return T <= 32 || (T <= 64 && (dtype == GIFT_FP32 || (int64_t)d * f <= (int64_t)1 << 24));
 }
 hipError_t launch_glu_tokens(const GluCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s);

@@ -23,10 +23,9 @@ struct Matrix {
   int64_t ld, rows;
   int64_t cols, size;
   bool ok() const { return rows == 0 || (p && aligned_to(p, (size_t)size) && ld >= cols); }
-  // as the products read it (see gift_glu_workspace_bytes)
-  bool rows16() const {
-    return aligned_to(p, 16) && (rows <= 1 || (ld * size % 16 == 0 && ld * size <= gift::kProductRow));
-  }
+  // what the products need to read it as it is
+  bool near() const { return rows <= 1 || ld * size <= gift::kProductRow; }
+  bool rows16() const { return near() && aligned_to(p, 16) && (rows <= 1 || ld * size % 16 == 0); }
   __int128 begin() const { return (__int128)reinterpret_cast<uintptr_t>(p); }
   __int128 end() const { return begin() + ((__int128)(rows - 1) * ld + cols) * size; }
 };
@@ -179,7 +178,7 @@ size_t gift_glu_backward_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_
   c.T = T;
   c.d = d;
   c.f = f;
-  c.aligned = aligned != 0;
+  c.aligned = c.near = aligned != 0;
   return gift::glu_backward_workspace(c);
 }
 
@@ -206,7 +205,8 @@ gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int6
       if (!disjoint(i, dx) || !disjoint(i, dz) || !disjoint(i, du)) return GIFT_ERR_INVALID_ARG;
     if (!disjoint(dz, dx) || !disjoint(du, dx)) return GIFT_ERR_INVALID_ARG;
     if (f > kProductCols || !reach(d, T, T, f)) return GIFT_ERR_UNSUPPORTED;
-    c.aligned = wg.rows16() && wu.rows16() && dz.rows16() && du.rows16() && (f == 1 || ldg == ldu) && (T == 1 || lddz == lddup);
+    c.aligned = dz.rows16() && du.rows16() && (T == 1 || lddz == lddup);
+    c.near = wg.near() && wu.near() && (f == 1 || ldg == ldu);
   }
   if ((h_drop && T > kDropRows) || gift::glu_gradients_grid(T, f) > kMaxGrid) return GIFT_ERR_UNSUPPORTED;
   c.act = act;
@@ -247,7 +247,7 @@ size_t gift_weight_grad_x_workspace_bytes(int64_t T, int32_t m, int32_t d, int32
   c.T = T;
   c.m = m;
   c.d = d;
-  c.aligned = aligned != 0;
+  c.near = aligned != 0;
   return gift::wgrad_x_workspace(c);
 }
 
@@ -272,7 +272,7 @@ gift_status gift_weight_grad_x(const void* d_delta, int32_t dtype, int64_t ldd, 
   c.accumulate = accumulate ? 1 : 0;
   c.W = d_W;
   c.ldw = ldw;
-  c.aligned = delta.rows16() && x.rows16();
+  c.near = delta.near() && x.near();
   c.work = d_work;
   const size_t need = gift::wgrad_x_workspace(c);
   if (need && (!d_work || !aligned_to(d_work, 16))) return GIFT_ERR_INVALID_ARG;

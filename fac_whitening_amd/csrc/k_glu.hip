@@ -8,9 +8,28 @@
 
 namespace gift {
 
-// dgate and dup: eight columns of a row a thread.
+// Eight of a row's rounded values (v: before the rounding, exact for fp32) as
+// k_product_pack lays them out, zeros past the row's end.
+template <typename T>
+__device__ __forceinline__ void lay_out(const Raw8<T>& r, float* v, uint16_t* dst, int64_t t, int j, int nb, int64_t rows, int n) {
+  uint16_t* p = dst + (t * nb * 8 + j);
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < n ? r.w[i] : 2 * i < n ? r.w[i] & 0xFFFFu : 0u;
+    store_words<4>(p, w, false);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? v[i] : 0.f;
+    split_planes(v, [&](int pl, const uint32_t* w) { store_words<4>(p + pl * rows * nb * 8, w, false); });
+  }
+}
+
+// dgate and dup: eight columns of a row a thread; pz and pu: also laid out for
+// the product that follows.
 template <typename T, int ACT>
-__global__ void __launch_bounds__(256) k_glu_gradients(GluGradCall c, DropArgs drop, int nb, int64_t n) {
+__global__ void __launch_bounds__(256) k_glu_gradients(GluGradCall c, DropArgs drop, int nb, int64_t n,
+                                                       uint16_t* pz, uint16_t* pu) {
   const int64_t first = (int64_t)blockIdx.x * 256;
   const int64_t t0 = first / nb;
   if (first + threadIdx.x >= n) return;
@@ -38,8 +57,10 @@ __global__ void __launch_bounds__(256) k_glu_gradients(GluGradCall c, DropArgs d
   Raw8<T> o;
   pack8(z, o);
   store8(static_cast<T*>(c.dgate) + t * c.lddz + j, o, m, false);
+  if (pz) lay_out(o, z, pz, t, j, nb, c.T, m);
   pack8(u, o);
   store8(static_cast<T*>(c.dup) + t * c.lddup + j, o, m, false);
+  if (pz) lay_out(o, u, pu, t, j, nb, c.T, m);
 }
 
 // W = 0: the gradient of no tokens.
@@ -75,9 +96,9 @@ ProductCall glu_product(const GluCall& c) {
   p.act = c.act;
   p.dtype = c.dtype;
   p.parts = 1;
-  p.a[0] = {c.wg, c.ldg, c.f, c.d, c.aligned};
-  p.a[1] = {c.wu, c.ldu, c.f, c.d, c.aligned};
-  p.b[0] = {c.x, c.ldx, c.T, c.d, c.aligned};
+  p.a[0] = {c.wg, c.ldg, c.f, c.d, c.aligned, false, false};
+  p.a[1] = {c.wu, c.ldu, c.f, c.d, c.aligned, false, false};
+  p.b[0] = {c.x, c.ldx, c.T, c.d, c.aligned, false, false};
   p.M = c.f;
   p.N = c.T;
   p.K = c.d;
@@ -91,21 +112,31 @@ ProductCall glu_product(const GluCall& c) {
   return p;
 }
 
+bool gradients_packed(const GluGradCall& c) { return c.dtype == GIFT_FP32 || c.f % 8 != 0 || !c.aligned; }
+
 ProductCall dx_product(const GluGradCall& c) {
   ProductCall p{};
+  p.work = c.work;
   p.epi = kEpiStore;
   p.dtype = c.dtype;
   p.parts = 2;
-  p.a[0] = {c.wg, c.ldg, c.f, c.d, c.aligned};
-  p.a[1] = {c.wu, c.ldu, c.f, c.d, c.aligned};
-  p.b[0] = {c.dgate, c.lddz, c.T, c.f, c.aligned};
-  p.b[1] = {c.dup, c.lddup, c.T, c.f, c.aligned};
+  p.a[0] = {c.wg, c.ldg, c.f, c.d, false, c.near, false};
+  p.a[1] = {c.wu, c.ldu, c.f, c.d, false, c.near, false};
+  p.b[0] = {c.dgate, c.lddz, c.T, c.f, c.aligned, false, false};
+  p.b[1] = {c.dup, c.lddup, c.T, c.f, c.aligned, false, false};
+  if (gradients_packed(c)) {
+    // k_glu_gradients lays them out in front of the workspace
+    char* w = static_cast<char*>(c.work);
+    const size_t bytes = product_packed(c.dtype, c.T, c.f);
+    p.b[0] = {w, 0, c.T, c.f, false, false, true};
+    p.b[1] = {w + bytes, 0, c.T, c.f, false, false, true};
+    p.work = w + 2 * bytes;
+  }
   p.M = c.d;
   p.N = c.T;
   p.K = c.f;
   p.out = c.dx;
   p.ldo = c.lddx;
-  p.work = c.work;
   return p;
 }
 
@@ -114,8 +145,8 @@ ProductCall grad_product(const WgradXCall& c) {
   p.epi = kEpiGrad;
   p.dtype = c.dtype;
   p.parts = 1;
-  p.a[0] = {c.x, c.ldx, c.T, c.d, c.aligned};
-  p.b[0] = {c.delta, c.ldd, c.T, c.m, c.aligned};
+  p.a[0] = {c.x, c.ldx, c.T, c.d, false, c.near, false};
+  p.b[0] = {c.delta, c.ldd, c.T, c.m, false, c.near, false};
   p.M = c.d;
   p.N = c.m;
   p.K = c.T;
@@ -130,7 +161,10 @@ ProductCall grad_product(const WgradXCall& c) {
 }  // namespace
 
 size_t glu_forward_workspace(const GluCall& c) { return glu_by_tokens(c.dtype, c.T, c.d, c.f) ? 0 : product_workspace(glu_product(c)); }
-size_t glu_backward_workspace(const GluGradCall& c) { return c.T ? product_workspace(dx_product(c)) : 0; }
+size_t glu_backward_workspace(const GluGradCall& c) {
+  if (c.T == 0) return 0;
+  return product_workspace(dx_product(c)) + (gradients_packed(c) ? 2 * product_packed(c.dtype, c.T, c.f) : 0);
+}
 size_t wgrad_x_workspace(const WgradXCall& c) { return c.T ? product_workspace(grad_product(c)) : 0; }
 
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s) {
@@ -140,10 +174,15 @@ hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_
 
 hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s) {
   if (c.T == 0) return hipSuccess;
+  uint16_t* planes[2] = {nullptr, nullptr};
+  if (c.dx && gradients_packed(c)) {
+    planes[0] = static_cast<uint16_t*>(c.work);
+    planes[1] = planes[0] + product_packed(c.dtype, c.T, c.f) / 2;
+  }
   with_type(c.dtype, [&](auto t) {
     with_act(c.act, [&](auto a) {
       hipLaunchKernelGGL((k_glu_gradients<decltype(t), decltype(a)::value>), dim3((unsigned)glu_gradients_grid(c.T, c.f)),
-                         dim3(256), 0, s, c, drop, (int)cdiv(c.f, 8), c.T * cdiv(c.f, 8));
+                         dim3(256), 0, s, c, drop, (int)cdiv(c.f, 8), c.T * cdiv(c.f, 8), planes[0], planes[1]);
     });
   });
   if (c.dx) return launch_product(dx_product(c), DropArgs{}, s);

@@ -74,9 +74,10 @@ __global__ void __launch_bounds__(64 * kTokenWaves) k_glu_tokens(GluCall c, Drop
     u[r] = static_cast<const T*>(c.wu) + (int64_t)fr * c.ldu;
   }
   const T* x[NT];
+  const int t0 = blockIdx.y * TOK;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int64_t t = 16 * n + row < c.T ? 16 * n + row : c.T - 1;
+    const int64_t t = t0 + 16 * n + row < c.T ? t0 + 16 * n + row : c.T - 1;
     x[n] = static_cast<const T*>(c.x) + t * c.ldx;
   }
   tf32x4 z[R][NT], v[R][NT];
@@ -154,15 +155,16 @@ __global__ void __launch_bounds__(64 * kTokenWaves) k_glu_tokens(GluCall c, Drop
       *reinterpret_cast<tf32x4*>(&part[wave][1][16 * n + row][16 * r + 4 * kq]) = v[r][n];
     }
   __syncthreads();
-  const int t = threadIdx.x / (2 * R), h = threadIdx.x % (2 * R) * 8;
-  if (t >= c.T || t >= TOK || f0 + h >= c.f) return;
+  const int tt = threadIdx.x / (2 * R), h = threadIdx.x % (2 * R) * 8;
+  const int64_t t = t0 + tt;
+  if (t >= c.T || tt >= TOK || f0 + h >= c.f) return;
   float zz[8] = {}, vv[8] = {};
 #pragma unroll
   for (int w = 0; w < kTokenWaves; ++w)
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-      const tf32x4 a = *reinterpret_cast<const tf32x4*>(&part[w][0][t][h + i]);
-      const tf32x4 b = *reinterpret_cast<const tf32x4*>(&part[w][1][t][h + i]);
+      const tf32x4 a = *reinterpret_cast<const tf32x4*>(&part[w][0][tt][h + i]);
+      const tf32x4 b = *reinterpret_cast<const tf32x4*>(&part[w][1][tt][h + i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         zz[i + j] += a[j];
@@ -200,12 +202,14 @@ void tokens_rows(const GluCall& c, const DropArgs& drop, hipStream_t s) {
       hipLaunchKernelGGL((k_glu_tokens<T, ACT, NT, 2>), dim3((unsigned)cdiv(c.f, 32)), block, 0, s, c, drop);
       return;
     }
-  hipLaunchKernelGGL((k_glu_tokens<T, ACT, NT, 1>), dim3((unsigned)cdiv(c.f, 16)), block, 0, s, c, drop);
+  // (fp32: 32 tokens at a time)
+  hipLaunchKernelGGL((k_glu_tokens<T, ACT, NT, 1>), dim3((unsigned)cdiv(c.f, 16), (unsigned)cdiv(c.T, 16 * NT)), block, 0, s, c,
+                     drop);
 }
 template <typename T, int ACT>
 void tokens_go(const GluCall& c, const DropArgs& drop, hipStream_t s) {
   if (c.T <= 16) tokens_rows<T, ACT, 1>(c, drop, s);
-  else if (c.T <= 32) tokens_rows<T, ACT, 2>(c, drop, s);
+  else if (c.T <= 32 || sizeof(T) == 4) tokens_rows<T, ACT, 2>(c, drop, s);
   else if constexpr (sizeof(T) == 2) tokens_rows<T, ACT, 4>(c, drop, s);
 }
 template <typename T>

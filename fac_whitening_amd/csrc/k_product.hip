@@ -197,12 +197,12 @@ __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
   uint32_t za = 0, zu = 0, zb = 0;
   int xoff[NS ? NS : 1];
   uint32_t ldx2[NS ? NS : 1];
-  int64_t xbytes[NS ? NS : 1];   // of a row, whole chunks
+  int64_t xbytes[NS ? NS : 1];   // of a row
   if constexpr (X) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       ldx2[n] = side_of(n) ? ldb2 : lda2;
-      xbytes[n] = 2 * (((side_of(n) ? ka->N : (int64_t)ka->M) + 7) & ~(int64_t)7);
+      xbytes[n] = 2 * (side_of(n) ? ka->bcols : ka->acols);
     }
   }
   int li = 0, lj = 0;
@@ -694,17 +694,27 @@ __global__ void __launch_bounds__(256) k_product_join(ProdArgs a, ProdOut o, int
   }
 }
 
-// An operand laid out anew: rows 16-byte aligned, padded with zeros to a
+// Operands laid out anew: rows 16-byte aligned, padded with zeros to a
 // multiple of 8 columns; an fp32 operand as three bf16 planes (split_planes).
+struct PackArgs {
+  const void* src[4];
+  uint16_t* dst[4];
+  int64_t ld[4], rows[4], block[5];   // block: first workgroup of each operand
+  int cols[4];
+};
 template <typename T>
-__global__ void __launch_bounds__(256) k_product_pack(const T* src, int64_t ld, int64_t rows, int cols, uint16_t* dst,
-                                                      int64_t ldp, int nb) {
-  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = k / nb;
+__global__ void __launch_bounds__(256) k_product_pack(PackArgs a) {
+  int m = 0;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m += blockIdx.x >= a.block[i];
+  const int cols = a.cols[m], nb = (cols + 7) / 8;
+  const int64_t first = ((int64_t)blockIdx.x - a.block[m]) * 256, r0 = first / nb;
+  const uint32_t at = (uint32_t)(first - r0 * nb) + threadIdx.x, down = at / (uint32_t)nb;
+  const int64_t r = r0 + down, rows = a.rows[m], ldp = (int64_t)nb * 8;
   if (r >= rows) return;
-  const int c = (int)(k - r * nb) * 8;
-  const Raw8<T> x = load8(src + r * ld + c, cols - c);
-  uint16_t* p = dst + r * ldp + c;
+  const int c = (int)(at - down * (uint32_t)nb) * 8;
+  const Raw8<T> x = load8(static_cast<const T*>(a.src[m]) + r * a.ld[m] + c, cols - c);
+  uint16_t* p = a.dst[m] + r * ldp + c;
   if constexpr (sizeof(T) == 2) {
     store_words<4>(p, x.w, false);
   } else {
@@ -816,60 +826,73 @@ void product_types(const ProductCall& c, const ProdArgs& a, const ProdOut& o, co
 
 int planes_of(int dtype) { return dtype == GIFT_FP32 ? 3 : 1; }
 int64_t packed_ld(int64_t cols) { return cdiv(cols, 8) * 8; }
-size_t packed_bytes(const ProdOperand& m, int dtype) {
-  return align256((size_t)planes_of(dtype) * (size_t)m.rows * (size_t)packed_ld(m.cols) * 2);
-}
-bool as_it_is(const ProdOperand& m, int dtype) {
-  return dtype != GIFT_FP32 && m.cols % 8 == 0 && m.aligned;
+// A direct operand is loaded in whole chunks of 8; a transposing one from any address, in whole words.
+bool as_it_is(const ProdOperand& m, int dtype, bool turned) {
+  if (dtype == GIFT_FP32 || m.packed) return false;
+  return turned ? m.near && m.cols % 2 == 0 : m.aligned && m.cols % 8 == 0;
 }
 
 }  // namespace
 
 int64_t product_tiles(int64_t M, int64_t N) { return cdiv(M, 64) * cdiv(N, 128); }
 
-// Workspace: the packed operands, one after another, then the pieces.
+size_t product_packed(int dtype, int64_t rows, int64_t cols) {
+  return align256((size_t)planes_of(dtype) * (size_t)rows * (size_t)packed_ld(cols) * 2);
+}
+
+// Workspace: the operands to pack, one after another, then the pieces.
 size_t product_workspace(const ProductCall& c) {
+  const bool ax = c.epi != kEpiGlu, bx = c.epi == kEpiGrad;
   size_t b = 0;
-  const ProdOperand* m[6] = {&c.a[0], &c.a[1], &c.b[0], &c.b[1]};
-  for (int i = 0; i < 4; ++i)
-    if (m[i]->rows && !as_it_is(*m[i], c.dtype)) b += packed_bytes(*m[i], c.dtype);
-  const ProdPlan p = product_plan(c.epi, c.epi != kEpiGlu, c.epi == kEpiGrad, c.M, c.N, c.K,
-                                  c.parts * (c.dtype == GIFT_FP32 ? 6 : 1));
-  return b + align256(p.bytes);
+  for (int i = 0; i < 2; ++i) {
+    if (c.a[i].rows && !c.a[i].packed && !as_it_is(c.a[i], c.dtype, ax)) b += product_packed(c.dtype, c.a[i].rows, c.a[i].cols);
+    if (c.b[i].rows && !c.b[i].packed && !as_it_is(c.b[i], c.dtype, bx)) b += product_packed(c.dtype, c.b[i].rows, c.b[i].cols);
+  }
+  return b + align256(product_plan(c.epi, ax, bx, c.M, c.N, c.K, c.parts * (c.dtype == GIFT_FP32 ? 6 : 1)).bytes);
 }
 
 hipError_t launch_product(const ProductCall& c, const DropArgs& drop, hipStream_t s) {
+  const bool ax = c.epi != kEpiGlu, bx = c.epi == kEpiGrad;
   ProdArgs a{};
   char* work = static_cast<char*>(c.work);
-  // operands as the kernel reads them: first plane, distance of the planes, leading dimension
+  // operands as the kernel reads them: first plane, distance of the planes, leading dimension, columns
   struct Laid {
     uint64_t p;
-    int64_t plane, ld;
+    int64_t plane, ld, cols;
   };
-  auto lay = [&](const ProdOperand& m) {
+  PackArgs pack{};
+  int packs = 0;
+  int64_t blocks = 0;
+  auto lay = [&](const ProdOperand& m, bool turned) {
     Laid l{};
     if (!m.rows) return l;
-    if (as_it_is(m, c.dtype)) {
-      l.p = (uint64_t)m.p;
-      l.ld = m.rows == 1 ? packed_ld(m.cols) : m.ld;
+    l.cols = packed_ld(m.cols);
+    l.ld = l.cols;
+    l.plane = m.rows * l.ld * 2;
+    l.p = (uint64_t)m.p;
+    if (m.packed) return l;
+    if (as_it_is(m, c.dtype, turned)) {
+      if (m.rows > 1) l.ld = m.ld;
+      l.cols = m.cols;
       return l;
     }
     l.p = (uint64_t)work;
-    l.ld = packed_ld(m.cols);
-    l.plane = m.rows * l.ld * 2;
-    const int nb = (int)(l.ld / 8);
-    const dim3 grid((unsigned)cdiv(m.rows * nb, 256));
-    uint16_t* dst = reinterpret_cast<uint16_t*>(work);
-    if (c.dtype == GIFT_FP32)
-      hipLaunchKernelGGL(k_product_pack<float>, grid, dim3(256), 0, s, static_cast<const float*>(m.p), m.ld, m.rows, (int)m.cols,
-                         dst, l.ld, nb);
-    else
-      hipLaunchKernelGGL(k_product_pack<Bf16>, grid, dim3(256), 0, s, static_cast<const Bf16*>(m.p), m.ld, m.rows, (int)m.cols, dst,
-                         l.ld, nb);
-    work += packed_bytes(m, c.dtype);
+    pack.src[packs] = m.p;
+    pack.dst[packs] = reinterpret_cast<uint16_t*>(work);
+    pack.ld[packs] = m.ld;
+    pack.rows[packs] = m.rows;
+    pack.cols[packs] = (int)m.cols;
+    pack.block[packs++] = blocks;
+    blocks += cdiv(m.rows * (l.ld / 8), 256);
+    work += product_packed(c.dtype, m.rows, m.cols);
     return l;
   };
-  const Laid A[2] = {lay(c.a[0]), lay(c.a[1])}, B[2] = {lay(c.b[0]), lay(c.b[1])};
+  const Laid A[2] = {lay(c.a[0], ax), lay(c.a[1], ax)}, B[2] = {lay(c.b[0], bx), lay(c.b[1], bx)};
+  for (int i = packs; i < 5; ++i) pack.block[i] = blocks;
+  if (packs) {
+    if (c.dtype == GIFT_FP32) hipLaunchKernelGGL(k_product_pack<float>, dim3((unsigned)blocks), dim3(256), 0, s, pack);
+    else hipLaunchKernelGGL(k_product_pack<Bf16>, dim3((unsigned)blocks), dim3(256), 0, s, pack);
+  }
   // of the nine products of planes the six largest, the smallest of them first
   static const int kPlanes[6][2] = {{0, 2}, {1, 1}, {2, 0}, {0, 1}, {1, 0}, {0, 0}};
   const int n = c.dtype == GIFT_FP32 ? 6 : 1;
@@ -884,6 +907,8 @@ hipError_t launch_product(const ProductCall& c, const DropArgs& drop, hipStream_
   a.lda = A[0].ld;
   a.lda2 = A[1].ld;
   a.ldb = B[0].ld;
+  a.acols = A[0].cols;
+  a.bcols = B[0].cols;
   a.K = c.K;
   a.M = (int)c.M;
   a.N = c.N;

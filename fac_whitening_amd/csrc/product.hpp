@@ -98,6 +98,7 @@ struct ProdArgs {
   int64_t K;            // of a segment
   int nst;              // stages of 64 of a segment
   int64_t lda, lda2, ldb;
+  int64_t acols, bcols; // of a transposing operand's rows: all that may be read
   int M;                // outputs along i
   int64_t N;            // and along j
   int nbm, nbn, unit;   // tiles along i and j; tiles are split at multiples of `unit` stages
@@ -120,6 +121,8 @@ struct ProdOperand {
   const void* p;
   int64_t ld, rows, cols;
   bool aligned;         // rows 16-byte aligned and at most kProductRow bytes apart
+  bool near;            // rows at most kProductRow bytes apart
+  bool packed;          // p is what k_product_pack makes of such an operand
 };
 
 // A product of the gated block's (see kEpi*): `parts` pairs of operands, each
@@ -136,6 +139,7 @@ struct ProductCall {
 };
 constexpr int64_t kProductRow = (int64_t)1 << 22;   // bytes: 256 rows' offsets stay below 2^31
 int64_t product_tiles(int64_t M, int64_t N);
+size_t product_packed(int dtype, int64_t rows, int64_t cols);   // bytes of an operand laid out anew
 size_t product_workspace(const ProductCall& c);
 hipError_t launch_product(const ProductCall& c, const DropArgs& drop, hipStream_t s);
 
