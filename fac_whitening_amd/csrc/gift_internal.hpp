@@ -321,6 +321,7 @@ struct GluGradCall {
   int64_t lddx;
   bool aligned;         // rows of dgate and dup (see ProdOperand), both the same distance apart
   bool near;            // rows of the weights, both the same distance apart
+  bool in_place;        // an output shares memory with dh, gate or up
   void* work;
 };
 struct WgradXCall {
@@ -353,6 +354,12 @@ inline bool glu_by_tokens(int dtype, int64_t T, int d, int f) {
 }
 hipError_t launch_glu_tokens(const GluCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s);
+// Whether the tokens' backward form runs: dx asked for, few rows, and no output over what it reads again.
+inline bool glu_backward_by_tokens(const GluGradCall& c) {
+  return c.T <= (c.dtype == GIFT_FP32 ? 16 : 32) && !c.in_place;
+}
+size_t glu_tokens_backward_workspace(int64_t T, int d, int f);
+hipError_t launch_glu_tokens_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_wgrad_x(const WgradXCall& c, hipStream_t s);
 

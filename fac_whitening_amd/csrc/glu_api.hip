@@ -179,7 +179,10 @@ size_t gift_glu_backward_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_
   c.d = d;
   c.f = f;
   c.aligned = c.near = aligned != 0;
-  return gift::glu_backward_workspace(c);
+  const size_t apart = gift::glu_backward_workspace(c);
+  c.in_place = true;
+  const size_t over = gift::glu_backward_workspace(c);
+  return apart > over ? apart : over;
 }
 
 gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int64_t lddh, int64_t T, int32_t f,
@@ -197,6 +200,7 @@ gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int6
     if (!in_place_or_disjoint(i, dz) || !in_place_or_disjoint(i, du)) return GIFT_ERR_INVALID_ARG;
   if (!disjoint(dz, du)) return GIFT_ERR_INVALID_ARG;
   gift::GluGradCall c{};
+  for (const void* i : {d_dh, d_gate, d_up}) c.in_place = c.in_place || i == d_dgate || i == d_dup;
   if (d_dx) {
     if (!cols_ok(d)) return GIFT_ERR_INVALID_ARG;
     const Matrix wg{d_wg, ldg, f, d, size}, wu{d_wu, ldu, f, d, size}, dx{d_dx, lddx, T, d, size};
@@ -204,6 +208,7 @@ gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int6
     for (const Matrix& i : {wg, wu})
       if (!disjoint(i, dx) || !disjoint(i, dz) || !disjoint(i, du)) return GIFT_ERR_INVALID_ARG;
     if (!disjoint(dz, dx) || !disjoint(du, dx)) return GIFT_ERR_INVALID_ARG;
+    for (const Matrix& i : {dh, z, u}) c.in_place = c.in_place || !disjoint(i, dx);
     if (f > kProductCols || !reach(d, T, T, f)) return GIFT_ERR_UNSUPPORTED;
     c.aligned = dz.rows16() && du.rows16() && (T == 1 || lddz == lddup);
     c.near = wg.near() && wu.near() && (f == 1 || ldg == ldu);

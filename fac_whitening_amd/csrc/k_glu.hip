@@ -163,6 +163,7 @@ ProductCall grad_product(const WgradXCall& c) {
 size_t glu_forward_workspace(const GluCall& c) { return glu_by_tokens(c.dtype, c.T, c.d, c.f) ? 0 : product_workspace(glu_product(c)); }
 size_t glu_backward_workspace(const GluGradCall& c) {
   if (c.T == 0) return 0;
+  if (glu_backward_by_tokens(c)) return glu_tokens_backward_workspace(c.T, c.d, c.f);
   return product_workspace(dx_product(c)) + (gradients_packed(c) ? 2 * product_packed(c.dtype, c.T, c.f) : 0);
 }
 size_t wgrad_x_workspace(const WgradXCall& c) { return c.T ? product_workspace(grad_product(c)) : 0; }
@@ -174,6 +175,7 @@ hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_
 
 hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s) {
   if (c.T == 0) return hipSuccess;
+  if (c.dx && glu_backward_by_tokens(c)) return launch_glu_tokens_backward(c, drop, s);
   uint16_t* planes[2] = {nullptr, nullptr};
   if (c.dx && gradients_packed(c)) {
     planes[0] = static_cast<uint16_t*>(c.work);

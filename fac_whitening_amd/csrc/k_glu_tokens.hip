@@ -13,52 +13,6 @@
 
 namespace gift {
 
-typedef float tf32x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ tf32x4 mfma16(const pbf16x8& a, const pbf16x8& b, const tf32x4& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ tf32x4 mfma16(const pf16x8& a, const pf16x8& b, const tf32x4& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-
-// Eight elements as operands: themselves, or an fp32's three planes.
-template <typename T>
-struct Planes {
-  static constexpr int P = sizeof(T) == 4 ? 3 : 1;
-  Frag8<T> v[P];
-};
-template <typename T>
-__device__ __forceinline__ Planes<T> planes(const Raw8<T>& r) {
-  Planes<T> o;
-  if constexpr (sizeof(T) == 2) {
-    o.v[0] = __builtin_bit_cast(Frag8<T>, r.w);
-  } else {
-    float v[8];
-    unpack8(r, v);
-    split_planes(v, [&](int p, const uint32_t* w) {
-      const pu32x4 u = {w[0], w[1], w[2], w[3]};
-      o.v[p] = __builtin_bit_cast(pbf16x8, u);
-    });
-  }
-  return o;
-}
-template <typename T>
-__device__ __forceinline__ tf32x4 multiply(const Planes<T>& a, const Planes<T>& b, tf32x4 c) {
-  if constexpr (sizeof(T) == 2) {
-    return mfma16(a.v[0], b.v[0], c);
-  } else {
-    c = mfma16(a.v[0], b.v[2], c);
-    c = mfma16(a.v[1], b.v[1], c);
-    c = mfma16(a.v[2], b.v[0], c);
-    c = mfma16(a.v[0], b.v[1], c);
-    c = mfma16(a.v[1], b.v[0], c);
-    return mfma16(a.v[0], b.v[0], c);
-  }
-}
-
-constexpr int kTokenWaves = 8;
-
 template <typename T, int ACT, int NT, int R>
 __global__ void __launch_bounds__(64 * kTokenWaves) k_glu_tokens(GluCall c, DropArgs drop) {
   constexpr int TOK = 16 * NT, PITCH = 16 * R + 4;   // (floats of a token's hidden units)
@@ -116,16 +70,16 @@ __global__ void __launch_bounds__(64 * kTokenWaves) k_glu_tokens(GluCall c, Drop
   auto multiply_block = [&](const Block& b) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      Planes<T> px[NT];
+      OperandPlanes<T> px[NT];
 #pragma unroll
-      for (int m = 0; m < NT; ++m) px[m] = planes(b.x[s][m]);
+      for (int m = 0; m < NT; ++m) px[m] = operand_planes(b.x[s][m]);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const Planes<T> pg = planes(b.g[s][r]), pu = planes(b.u[s][r]);
+        const OperandPlanes<T> pg = operand_planes(b.g[s][r]), pu = operand_planes(b.u[s][r]);
 #pragma unroll
         for (int m = 0; m < NT; ++m) {
-          z[r][m] = multiply(pg, px[m], z[r][m]);
-          v[r][m] = multiply(pu, px[m], v[r][m]);
+          z[r][m] = multiply_planes(pg, px[m], z[r][m]);
+          v[r][m] = multiply_planes(pu, px[m], v[r][m]);
         }
       }
     }

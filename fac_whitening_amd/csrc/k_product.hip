@@ -741,9 +741,9 @@ struct ProdPlan {
 // x 6144 and 4096 x 4096, 128 to 8192 tokens), within a fifth or so:
 //   a stage of a workgroup   256: 1.75 each; 128: 1.0, 1.25, 1.15; deep: 0.6
 //   a whole tile written     256: 6, fp32 gradients 14; 128: 2, 4
-//   a piece written          256: 10, 128: 6
-//   the join                 5 with its launch, pieces at 8 TB/s, outputs at 6
-double product_try(ProdPlan& p, int side, int deep, int unit, int epi, bool ax, bool bx, int64_t M, int64_t N, int64_t K, int nseg) {
+//   a split                  7 for the launch of the join, pieces written and read at 8 TB/s, outputs written at 6, and
+//                            0.15 for each piece of a tile, which the join adds one after another
+double product_try(ProdPlan& p, int side, int deep, int unit, int most, int epi, bool ax, bool bx, int64_t M, int64_t N, int64_t K, int nseg) {
   p.side = side;
   p.deep = deep;
   p.nbm = (int)cdiv(M, epi == kEpiGlu ? side / 2 : side);
@@ -752,7 +752,9 @@ double product_try(ProdPlan& p, int side, int deep, int unit, int epi, bool ax, 
   p.grid = side == 128 && !deep ? 2 * kProductGroups : kProductGroups;
   const int total = p.nst * nseg;
   p.unit = unit ? unit : total;
-  const WLevel v = wgrad_levels(p.nbm * p.nbn, (int)cdiv(total, p.unit), p.grid);
+  const int64_t tiles = (int64_t)p.nbm * p.nbn;
+  if (unit && tiles * most < p.grid) p.grid = (int)tiles * most;
+  const WLevel v = wgrad_levels((int)tiles, (int)cdiv(total, p.unit), p.grid);
   const WSplit w = wgrad_split(v);
   p.first = w.first;
   p.split = w.tiles;
@@ -761,7 +763,7 @@ double product_try(ProdPlan& p, int side, int deep, int unit, int epi, bool ax, 
   const bool large = side == 256, grad = epi == kEpiGrad;
   const double stage = large ? 1.75 : deep ? 0.6 : bx ? 1.15 : ax ? 1.25 : 1.0;
   const double whole = (double)(v.C * (int64_t)p.unit / total) * (large ? grad ? 14.0 : 6.0 : grad ? 4.0 : 2.0);
-  const double join = (large ? 10.0 : 6.0) + 5.0 + (double)p.bytes / 8e6 +
+  const double join = 7.0 + 2.0 * (double)p.bytes / 8e6 + 0.15 * (double)cdiv(p.grid, tiles) +
                       (double)p.split * side * side * (grad ? 4 : 2) / 6e6;
   return stages * stage + whole + (p.split ? join : 0.0);
 }
@@ -772,14 +774,16 @@ ProdPlan product_plan(int epi, bool ax, bool bx, int64_t M, int64_t N, int64_t K
   if (K < 1) return best;
   for (int form = 0; form < 3; ++form) {   // 256, 128, 128 deep
     if (form == 2 && (ax || bx)) continue;
-    for (int unit = 0; unit <= 8; unit += unit ? unit : 2) {
-      ProdPlan p{};
-      const double t = product_try(p, form == 0 ? 256 : 128, form == 2, unit, epi, ax, bx, M, N, K, nseg);
-      if (best.side == 0 || t < least) {
-        best = p;
-        least = t;
+    for (int unit = 0; unit <= 8; unit += unit ? unit : 2)
+      for (int most = 4; most <= 256; most *= 4) {   // workgroups a tile
+        ProdPlan p{};
+        const double t = product_try(p, form == 0 ? 256 : 128, form == 2, unit, most, epi, ax, bx, M, N, K, nseg);
+        if (best.side == 0 || t < least) {
+          best = p;
+          least = t;
+        }
+        if (unit == 0) break;
       }
-    }
   }
   return best;
 }

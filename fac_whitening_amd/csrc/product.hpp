@@ -46,6 +46,57 @@ __device__ __forceinline__ void split_planes(float* v, F&& put) {
   }
 }
 
+typedef float tf32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ tf32x4 mfma16(const pbf16x8& a, const pbf16x8& b, const tf32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ tf32x4 mfma16(const pf16x8& a, const pf16x8& b, const tf32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Eight elements as operands: themselves, or an fp32's three planes.
+template <typename T>
+struct OperandPlanes {
+  static constexpr int P = sizeof(T) == 4 ? 3 : 1;
+  Frag8<T> v[P];
+};
+template <typename T>
+__device__ __forceinline__ OperandPlanes<T> operand_planes(const Raw8<T>& r) {
+  OperandPlanes<T> o;
+  if constexpr (sizeof(T) == 2) {
+    o.v[0] = __builtin_bit_cast(Frag8<T>, r.w);
+  } else {
+    float v[8];
+    unpack8(r, v);
+    split_planes(v, [&](int p, const uint32_t* w) {
+      const pu32x4 u = {w[0], w[1], w[2], w[3]};
+      o.v[p] = __builtin_bit_cast(pbf16x8, u);
+    });
+  }
+  return o;
+}
+template <typename T>
+__device__ __forceinline__ tf32x4 multiply_planes(const OperandPlanes<T>& a, const OperandPlanes<T>& b, tf32x4 c) {
+  if constexpr (sizeof(T) == 2) {
+    return mfma16(a.v[0], b.v[0], c);
+  } else {
+    c = mfma16(a.v[0], b.v[2], c);
+    c = mfma16(a.v[1], b.v[1], c);
+    c = mfma16(a.v[2], b.v[0], c);
+    c = mfma16(a.v[0], b.v[1], c);
+    c = mfma16(a.v[1], b.v[0], c);
+    return mfma16(a.v[0], b.v[0], c);
+  }
+}
+
+// The kernels of few tokens: waves of a workgroup.
+constexpr int kTokenWaves = 8;
+
+__device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_value(Bf16* p, float v) { p->v = __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ void store_value(Fp16* p, float v) { p->v = __builtin_bit_cast(uint16_t, (_Float16)v); }
+
 // f(integral_constant<int, B>) ... f(integral_constant<int, E - 1>)
 template <int B, int E, typename F>
 __device__ __forceinline__ void unrolled(F&& f) {
