@@ -70,12 +70,22 @@ gift::DropArgs drop_args(const gift_dropout* d) {
 }
 constexpr int64_t kDropRows = (int64_t)1 << 32;
 
-// What a product's launches reach: columns whose rows the kernel's 32-bit offsets span, tiles of the output, and rows
-// that may have to be laid out anew.
+// What a product's launches reach: columns whose rows the kernel's 32-bit offsets span, tiles of the output and their
+// stages (12 segments at most) in the counts of wgrad_levels, and operands that may have to be laid out anew.
 constexpr int kProductCols = (int)(gift::kProductRow / 2);
-bool reach(int64_t M, int64_t N, int64_t rows, int64_t cols) {
-  return M <= kProductCols && rows < ((int64_t)1 << 36) && gift::product_tiles(M, N) <= kMaxGrid &&
-         rows <= kMaxGrid * 256 / gift::cdiv(cols, 8);
+bool may_pack(int64_t rows, int64_t cols) {
+  return rows < ((int64_t)1 << 36) && gift::cdiv(rows * gift::cdiv(cols, 8), 256) <= kMaxGrid / 4;
+}
+bool reach(int64_t M, int64_t N, int64_t K) {
+  return gift::product_tiles(M, N) <= kMaxGrid && gift::cdiv(K, 64) * 12 < ((int64_t)1 << 30) &&
+         (__int128)gift::product_tiles(M, N) * gift::cdiv(K, 64) * 12 < ((__int128)1 << 38);
+}
+bool glu_reach(int64_t T, int32_t d, int32_t f) {
+  return d <= kProductCols && f <= kProductCols && may_pack(T, d) && may_pack(T, f) && may_pack(f, d) && reach(f, T, d) &&
+         reach(d, T, f);
+}
+bool grad_reach(int64_t T, int32_t m, int32_t d) {
+  return d <= kProductCols && m <= kProductCols && may_pack(T, d) && may_pack(T, m) && reach(d, m, T);
 }
 
 bool act_ok(int32_t a) { return a >= GIFT_ACT_SILU && a <= GIFT_ACT_SIGMOID; }
@@ -100,7 +110,7 @@ gift_status gift_dropout_apply(const gift_dropout* h_drop, const void* d_x, int3
 
 size_t gift_glu_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t dtype, int32_t aligned) {
   if (!rows_count_ok(T) || !cols_ok(d) || !cols_ok(f) || !dtype_ok(dtype)) return 0;
-  if (d > kProductCols || !reach(f, T, T, d)) return 0;
+  if (!glu_reach(T, d, f)) return 0;
   gift::GluCall c{};
   c.dtype = dtype;
   c.T = T;
@@ -139,7 +149,7 @@ gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_
       if (!disjoint(out[k], out[l])) return GIFT_ERR_INVALID_ARG;
   }
   if (h_drop && T > kDropRows) return GIFT_ERR_UNSUPPORTED;
-  if (d > kProductCols || !reach(f, T, T, d) || (h_ckpt && gift::act_grid(T, f) > kMaxGrid)) return GIFT_ERR_UNSUPPORTED;
+  if (!glu_reach(T, d, f) || (h_ckpt && gift::act_grid(T, f) > kMaxGrid)) return GIFT_ERR_UNSUPPORTED;
   gift::GluCall c{};
   c.act = act;
   c.dtype = dtype;
@@ -172,7 +182,7 @@ gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_
 
 size_t gift_glu_backward_workspace_bytes(int64_t T, int32_t d, int32_t f, int32_t dtype, int32_t aligned) {
   if (!rows_count_ok(T) || !cols_ok(d) || !cols_ok(f) || !dtype_ok(dtype)) return 0;
-  if (f > kProductCols || !reach(d, T, T, f)) return 0;
+  if (!glu_reach(T, d, f)) return 0;
   gift::GluGradCall c{};
   c.dtype = dtype;
   c.T = T;
@@ -209,7 +219,7 @@ gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int6
       if (!disjoint(i, dx) || !disjoint(i, dz) || !disjoint(i, du)) return GIFT_ERR_INVALID_ARG;
     if (!disjoint(dz, dx) || !disjoint(du, dx)) return GIFT_ERR_INVALID_ARG;
     for (const Matrix& i : {dh, z, u}) c.in_place = c.in_place || !disjoint(i, dx);
-    if (f > kProductCols || !reach(d, T, T, f)) return GIFT_ERR_UNSUPPORTED;
+    if (!glu_reach(T, d, f)) return GIFT_ERR_UNSUPPORTED;
     c.aligned = dz.rows16() && du.rows16() && (T == 1 || lddz == lddup);
     c.near = wg.near() && wu.near() && (f == 1 || ldg == ldu);
   }
@@ -246,7 +256,7 @@ gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int6
 
 size_t gift_weight_grad_x_workspace_bytes(int64_t T, int32_t m, int32_t d, int32_t dtype, int32_t aligned) {
   if (!rows_count_ok(T) || !cols_ok(d) || !cols_ok(m) || !dtype_ok(dtype)) return 0;
-  if (m > kProductCols || !reach(d, m, T, d) || !reach(d, m, T, m)) return 0;
+  if (!grad_reach(T, m, d)) return 0;
   gift::WgradXCall c{};
   c.dtype = dtype;
   c.T = T;
@@ -263,7 +273,7 @@ gift_status gift_weight_grad_x(const void* d_delta, int32_t dtype, int64_t ldd, 
   const int64_t size = dtype_size(dtype);
   const Matrix delta{d_delta, ldd, T, m, size}, x{d_x, ldx, T, d, size}, W{d_W, ldw, m, d, 4};
   if (!delta.ok() || !x.ok() || !W.ok() || !disjoint(delta, W) || !disjoint(x, W)) return GIFT_ERR_INVALID_ARG;
-  if (m > kProductCols || !reach(d, m, T, d) || !reach(d, m, T, m)) return GIFT_ERR_UNSUPPORTED;
+  if (!grad_reach(T, m, d)) return GIFT_ERR_UNSUPPORTED;
   gift::WgradXCall c{};
   c.delta = d_delta;
   c.dtype = dtype;

@@ -8,7 +8,11 @@
 // v_mfma_f32_16x16x32, tokens being the other operand, in 16s.  The next block's
 // loads are in flight while one is multiplied.  The partial sums of the waves
 // meet in LDS and are added in order.  fp32 operands are split into three bf16
-// numbers in registers (see k_product_pack); six products are added.
+// numbers in registers (split_planes); six products are added.
+// Measured: 1 token, 1536 x 6144 bf16 9.7 us (weights at a copy's rate 6.1), fp32
+// 23 (12.2); 16 tokens, 4096 x 16384 bf16 58 us (43.5; 4.6 TB/s).  A wave has 8 to 16 KB
+// of loads in flight; what is left is the loads of x, which every workgroup
+// repeats, and the sums' way through LDS.
 #include "product.hpp"
 
 namespace gift {

@@ -12,6 +12,8 @@
 // columns store them).  The waves' sums meet in LDS, the slabs' in the
 // workspace; both are added in order, the latter by a second launch.  fp32
 // operands are split into three bf16 numbers in registers.
+// Measured: 1 token, 91 x 16173 fp32 12 + 3 us of kernels (as tiles with their join
+// 18 + 73); 2 tokens, 73 x 2752 bf16 9 + 3.
 #include "product.hpp"
 
 namespace gift {

@@ -1,6 +1,49 @@
-// Matrix products of 16-bit operands on the matrix cores:
-//   out[j][i] = sum_k A[i][k] B[j][k]
-// i the contiguous index of the output.
+// The matrix products of the gated feed-forward block and of the weight
+// gradient from a whole activation:
+//   out[j][i] = sum_k A[i][k] B[j][k],  i the contiguous index of the output.
+//   kEpiGlu    A = Wg and Wu, B = x: z and u side by side, out = D(act(z) u)
+//   kEpiStore  A = Wg^T then Wu^T, B = dgate then dup: dx
+//   kEpiGrad   A = x^T, B = delta^T: the weight gradient
+// On v_mfma_f32_32x32x16 with fp32 sums.  bf16 and fp16 operands multiply
+// exactly.  An fp32 operand is three bf16 planes (split_planes) and the long
+// axis six segments, the products of planes (0, 2), (1, 1), (2, 0), (0, 1), (1,
+// 0), (0, 0): what is left out is below 2^-24 of |A| |B|, and the small products
+// are added before the large ones.
+//
+// One workgroup (4 waves, 2 x 2) makes a tile of 256 x 256, or 128 x 128, in
+// stages of 64 of the long axis; of kEpiGlu half of A's rows are the gate's,
+// half the up projection's, in turns of 32, so that a lane holds both sums of
+// an output.
+//  * Direct operands (rows of k) go from memory to LDS without registers, 16
+//    bytes a lane.  Transposing ones (rows of i or j: the weights in dx, both
+//    sides of the weight gradient) are loaded as blocks of 8 x 8, turned by
+//    v_perm and written as 16-byte operand vectors between the products; two
+//    stages of them are in flight in registers.  (The LDS's own transposing
+//    reads run at 48 bytes a clock; these products need 64.)  The lanes of a
+//    load are consecutive in memory: with the lanes along k instead, the address
+//    unit took 47 clocks a load in place of 16, and 8192^3 with both sides
+//    transposing 1063 us in place of 936.
+//  * Two stages in LDS, swizzled (chunk_slot; no bank conflicts).  A stage's
+//    products are 64 of 32 clocks a wave; the operands of the next 16 are read
+//    under them.  One barrier a stage, in front of the last 16: behind it the
+//    stage's buffer is free for the stage after next.  The loads run on
+//    through the workgroup's tiles: the next tile's first stages arrive under
+//    the epilogue.  Tiles of 128: two workgroups a compute unit, or one with four
+//    stages in LDS, whose loads have three stages' time to arrive (256 tokens,
+//    1536 x 6144: 23 us in place of 32).
+//  * A tile's outputs are turned in 4 KB of LDS a wave and written as rows of 128
+//    bytes, one block read back while the next one's activation is computed;
+//    outputs larger than the L2 caches past them (16384 x 6144, three outputs:
+//    775 -> 727 us; the order of the blocks 727 -> 657).
+//  * Tiles are shared among the workgroups in levels (wgrad_levels.hpp), pieces
+//    of split tiles joined in the order of the long axis by a second launch.
+// Measured (bf16): 8192^3 1.28 PFLOP/s direct, 1.20 transposing (a library
+// product 1.37, the clock then bound by power); 16384 tokens, 1536 x 6144:
+// forward 568 us, with both products kept and dropout 657, dx 530, weight
+// gradient 291.  Of dx, the matrix units are busy 59 % of 1.0 million clocks at 1.92
+// GHz; waves wait for counters and barriers 19 % of the time.  An earlier
+// barrier with all operands of a stage read at its start, and reads spread over
+// all products, took the same time.
 #include "product.hpp"
 
 namespace gift {
@@ -146,7 +189,7 @@ __device__ __forceinline__ void store16(TO* p, const uint32_t* w, int n, bool st
   }
 }
 
-// Products, E: operand type, TO: output type.
+// E: operand type, TO: output type, AX, BX: transposing sides, NBUF: stages in LDS, WGS: workgroups a compute unit.
 template <typename E, typename TO, int EPI, int ACT, int MT, int NT, bool AX, bool BX, int NBUF, int WGS>
 __global__ void __launch_bounds__(256, WGS) k_product(KernelArgs args) {
   const auto* const ka = &args.a;

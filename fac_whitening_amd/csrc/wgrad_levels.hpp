@@ -1,4 +1,4 @@
-// How the weight-gradient product (k_wgrad.hip) shares its output tiles among
+// How the products (k_wgrad.hip, k_product.hip) share their output tiles among
 // workgroups.  Plain integer arithmetic, the same on the host, which sizes the
 // workspace by it, and on the device.
 #pragma once
