@@ -304,7 +304,6 @@ struct GluCall {
   int64_t ldg, ldu;
   void *h, *gate, *up;
   int64_t ldh, ldz, ldup;
-  const gift_act_ckpt* ckpt;
   bool aligned;         // rows of x and the weights (see ProdOperand)
   void* work;
 };

@@ -168,7 +168,6 @@ gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_
   c.ldh = ldh;
   c.ldz = ldz;
   c.ldup = ldup;
-  c.ckpt = h_ckpt;
   c.aligned = x.rows16() && wg.rows16() && wu.rows16();
   c.work = d_work;
   const size_t need = gift::glu_forward_workspace(c);

@@ -68,8 +68,8 @@ __global__ void __launch_bounds__(256) k_glu_gradients(GluGradCall c, DropArgs d
 
 // W = 0: the gradient of no tokens.
 __global__ void __launch_bounds__(256) k_wgrad_none(float* W, int64_t ldw, int m, int d) {
-  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x, i = k / d;
-  if (i < m) W[i * ldw + (k - i * d)] = 0.f;
+  for (int i = blockIdx.x; i < m; i += gridDim.x)
+    for (int j = threadIdx.x; j < d; j += 256) W[i * ldw + j] = 0.f;
 }
 
 int64_t glu_gradients_grid(int64_t T, int f) { return cdiv(T * cdiv(f, 8), 256); }
@@ -197,7 +197,7 @@ hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipSt
 hipError_t launch_wgrad_x(const WgradXCall& c, hipStream_t s) {
   if (c.T == 0) {
     if (c.accumulate) return hipSuccess;
-    hipLaunchKernelGGL(k_wgrad_none, dim3((unsigned)cdiv((int64_t)c.m * c.d, 256)), dim3(256), 0, s, c.W, c.ldw, c.m, c.d);
+    hipLaunchKernelGGL(k_wgrad_none, dim3((unsigned)(c.m < 4096 ? c.m : 4096)), dim3(256), 0, s, c.W, c.ldw, c.m, c.d);
     return hipGetLastError();
   }
   return launch_product(grad_product(c), DropArgs{}, s);

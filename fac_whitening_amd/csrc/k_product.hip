@@ -129,15 +129,15 @@ __device__ __forceinline__ uint64_t uni64(uint64_t v) {
   return (uint64_t)(uint32_t)uni((int)(uint32_t)v) | (uint64_t)(uint32_t)uni((int)(uint32_t)(v >> 32)) << 32;
 }
 
+// A stage is 64 elements of the long axis, 128 bytes a row.
 template <int MT, int NT, int NBUF>
 struct PTile {
-  static constexpr int KT = 64;                                // elements of the long axis a stage
   static constexpr int SA = 64 * MT, SB = 64 * NT;             // rows of a tile's operands
   static constexpr int kBytesA = SA * 128, kBytesB = SB * 128, kStage = kBytesA + kBytesB;
   static constexpr int kTurn = 4096;                           // a wave's LDS for outputs
   static constexpr int kLds = NBUF * kStage + 4 * kTurn;
   static constexpr int LA = kBytesA / 4096, LB = kBytesB / 4096;   // direct loads of a wave a stage
-  static constexpr int KS = 4, PS = MT * NT;                   // steps of 16; products of a step
+  static constexpr int PS = MT * NT;                           // products of a step of 16
 };
 
 // Slot of 16-byte chunk c of row r of a stage (128 bytes).  A 16-byte LDS

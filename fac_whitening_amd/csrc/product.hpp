@@ -11,7 +11,6 @@ namespace gift {
 typedef __bf16 pbf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 pf16x8 __attribute__((ext_vector_type(8)));
 typedef float pf32x16 __attribute__((ext_vector_type(16)));
-typedef float pf32x4 __attribute__((ext_vector_type(4)));
 typedef int pi32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t pu32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t pu32x4 __attribute__((ext_vector_type(4)));
