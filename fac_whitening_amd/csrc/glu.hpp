@@ -100,7 +100,8 @@ __device__ __forceinline__ float act_value(float z, float* grad = nullptr) {
     const float w = k * (z + 0.044715f * z * z * z);
     float q;
     const float s = logistic(w, &q);
-    if (grad) *grad = s + z * (s * q) * (k * (1.f + 0.134145f * z * z));
+    // (where z^2 is infinite s q is zero, and 0 times an infinity is no number)
+    if (grad) *grad = s + z * (s * q) * (k * (1.f + 0.134145f * __builtin_fminf(z * z, 0x1p100f)));
     return z * s;
   }
 }
