@@ -1,11 +1,25 @@
-"""The activations of the gated block and their derivatives where squares and
-cubes of their arguments pass fp32's largest number."""
+"""The activations of the gated block and their derivatives over the whole
+range of a type: the tails, where both tend to zero, and values whose squares
+and cubes pass fp32's largest number.
+
+Tolerances.  U = 2^-24 is fp32's half step.  A value or derivative is a sum of
+terms of which each is off relative to itself: by (32 + 8 z^2 + 2 |z|^3) U, for
+  * some ten operations and hardware functions (1 ulp each): under 24 U;
+  * the normal tail's polynomial, 8 U (4.4e-7);
+  * an argument off by 4 U of itself, which moves e^-w by 4 |w| U: w = z (silu,
+    sigmoid), z^2 / 2 (gelu) or 1.6 |z| + 0.0714 |z|^3 (gelu_tanh).
+The terms are the derivative's own (terms() below), not larger ones.  A
+logistic value or exponential below 2^-126 may be zero: 2^-126 times what
+multiplies it is added."""
+import math
+
 import numpy as np
 import pytest
 import torch
+from scipy import special
 
 from oracle import feedforward as F
-from test_gpu_feedforward import ACTS, DEV, DT, f64
+from test_gpu_feedforward import ACTS, DEV, DT, U, check, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +28,34 @@ pytestmark = pytest.mark.gpu
 def fw():
     import fac_whitening_amd as fw
     return fw
+
+
+def relative(z):
+    z = np.abs(z)
+    return (32 + 8 * z ** 2 + 2 * z ** 3) * U
+
+
+def lost(z):
+    """What a number below 2^-126, taken as zero, is multiplied by at most."""
+    z = np.abs(z)
+    return 2.0 ** -126 * (1 + 1.6 * z * (1 + 0.135 * z ** 2))
+
+
+def terms(z, act):
+    """Magnitudes that act'(z) adds."""
+    s, q = special.expit(z), special.expit(-z)
+    if act == "relu":
+        return (z > 0) * 1.0
+    if act == "sigmoid":
+        return s * q
+    if act == "silu":
+        return s + np.abs(z) * s * q
+    if act == "gelu":
+        return special.ndtr(z) + np.abs(z) * np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    k = 2 * math.sqrt(2 / math.pi)
+    w = k * (z + 0.044715 * z ** 3)
+    s, q = special.expit(w), special.expit(-w)
+    return s + np.abs(z) * s * q * k * (1 + 3 * 0.044715 * z ** 2)
 
 
 def derivatives(fw, z, act, form):
@@ -42,6 +84,28 @@ def values(fw, z, act, form):
     torch.cuda.synchronize()
     assert (f64(up) == 1).all()
     return h.view(1, n), gate.view(1, n)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("form", ["pass", "tokens"])
+def test_derivatives_in_the_tails(fw, act, form):
+    z = torch.cat([torch.linspace(-30, 30, 6001, device=DEV), torch.linspace(-3, 3, 1001, device=DEV)])
+    Z = f64(z).reshape(1, -1)
+    a, da = F.act(Z, act)
+    dgate, dup = derivatives(fw, z, act, form)
+    check(dgate, da, relative(Z) * terms(Z, act) + lost(Z), act + " derivative")
+    check(dup, a, relative(Z) * np.abs(a) + lost(Z) * np.abs(Z), act)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("form", ["tiles", "tokens"])
+def test_values_in_the_tails(fw, act, form):
+    z = torch.linspace(-30, 30, 4001, device=DEV)
+    Z = f64(z).reshape(1, -1)
+    h, gate = values(fw, z, act, form)
+    assert np.array_equal(f64(gate), Z)
+    a = F.act(Z, act)[0]
+    check(h, a, relative(Z) * np.abs(a) + lost(Z) * (1 + np.abs(Z)), act)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
