@@ -345,6 +345,10 @@ int64_t glu_gradients_grid(int64_t T, int f);
 size_t glu_forward_workspace(const GluCall& c);
 size_t glu_backward_workspace(const GluGradCall& c);
 size_t wgrad_x_workspace(const WgradXCall& c);
+// Whether what a call lays out anew (the entries check its other sizes) is within a launch's reach.
+bool glu_forward_reach(const GluCall& c);
+bool glu_backward_reach(const GluGradCall& c);
+bool wgrad_x_reach(const WgradXCall& c);
 // Whether k_glu_tokens makes the block's output: up to 32 rows of x, and up to 64 where the weights are small (tokens
 // against tiles, 64 rows bf16: 1536 x 6144 22 and 23 us, 4096 x 16384 111 and 68) or fp32, whose tiles need their
 // operands laid out anew (1536 x 6144: 64 and 88).

@@ -2,7 +2,6 @@
 // gradient from a whole activation: argument checks, then the launches on the
 // caller's stream.  They keep no state.
 #include <cmath>
-#include <numeric>
 
 #include "product.hpp"
 
@@ -71,21 +70,17 @@ gift::DropArgs drop_args(const gift_dropout* d) {
 constexpr int64_t kDropRows = (int64_t)1 << 32;
 
 // What a product's launches reach: columns whose rows the kernel's 32-bit offsets span, tiles of the output and their
-// stages (12 segments at most) in the counts of wgrad_levels, and operands that may have to be laid out anew.
+// stages (12 segments at most) in the counts of wgrad_levels.  (Operands that are laid out anew: see product_reach.)
 constexpr int kProductCols = (int)(gift::kProductRow / 2);
-bool may_pack(int64_t rows, int64_t cols) {
-  return rows < ((int64_t)1 << 36) && gift::cdiv(rows * gift::cdiv(cols, 8), 256) <= kMaxGrid / 4;
-}
 bool reach(int64_t M, int64_t N, int64_t K) {
   return gift::product_tiles(M, N) <= kMaxGrid && gift::cdiv(K, 64) * 12 < ((int64_t)1 << 30) &&
          (__int128)gift::product_tiles(M, N) * gift::cdiv(K, 64) * 12 < ((__int128)1 << 38);
 }
 bool glu_reach(int64_t T, int32_t d, int32_t f) {
-  return d <= kProductCols && f <= kProductCols && may_pack(T, d) && may_pack(T, f) && may_pack(f, d) && reach(f, T, d) &&
-         reach(d, T, f);
+  return d <= kProductCols && f <= kProductCols && reach(f, T, d) && reach(d, T, f);
 }
 bool grad_reach(int64_t T, int32_t m, int32_t d) {
-  return d <= kProductCols && m <= kProductCols && may_pack(T, d) && may_pack(T, m) && reach(d, m, T);
+  return d <= kProductCols && m <= kProductCols && reach(d, m, T);
 }
 
 bool act_ok(int32_t a) { return a >= GIFT_ACT_SILU && a <= GIFT_ACT_SIGMOID; }
@@ -170,6 +165,7 @@ gift_status gift_glu_forward(int32_t act, const void* d_x, int32_t dtype, int64_
   c.ldup = ldup;
   c.aligned = x.rows16() && wg.rows16() && wu.rows16();
   c.work = d_work;
+  if (!gift::glu_forward_reach(c)) return GIFT_ERR_UNSUPPORTED;
   const size_t need = gift::glu_forward_workspace(c);
   if (need && (!d_work || !aligned_to(d_work, 16))) return GIFT_ERR_INVALID_ARG;
   if (work_bytes < need) return GIFT_ERR_WORKSPACE;
@@ -246,6 +242,7 @@ gift_status gift_glu_backward(int32_t act, const void* d_dh, int32_t dtype, int6
   c.lddx = lddx;
   c.work = d_work;
   if (d_dx) {
+    if (!gift::glu_backward_reach(c)) return GIFT_ERR_UNSUPPORTED;
     const size_t need = gift::glu_backward_workspace(c);
     if (need && (!d_work || !aligned_to(d_work, 16))) return GIFT_ERR_INVALID_ARG;
     if (work_bytes < need) return GIFT_ERR_WORKSPACE;
@@ -288,6 +285,7 @@ gift_status gift_weight_grad_x(const void* d_delta, int32_t dtype, int64_t ldd, 
   c.ldw = ldw;
   c.near = delta.near() && x.near();
   c.work = d_work;
+  if (!gift::wgrad_x_reach(c)) return GIFT_ERR_UNSUPPORTED;
   const size_t need = gift::wgrad_x_workspace(c);
   if (need && (!d_work || !aligned_to(d_work, 16))) return GIFT_ERR_INVALID_ARG;
   if (work_bytes < need) return GIFT_ERR_WORKSPACE;

@@ -170,6 +170,9 @@ size_t glu_backward_workspace(const GluGradCall& c) {
   return product_workspace(dx_product(c)) + (gradients_packed(c) ? 2 * product_packed(c.dtype, c.T, c.f) : 0);
 }
 size_t wgrad_x_workspace(const WgradXCall& c) { return c.T ? product_workspace(grad_product(c)) : 0; }
+bool glu_forward_reach(const GluCall& c) { return glu_by_tokens(c.dtype, c.T, c.d, c.f) || product_reach(glu_product(c)); }
+bool glu_backward_reach(const GluGradCall& c) { return glu_backward_by_tokens(c) || product_reach(dx_product(c)); }
+bool wgrad_x_reach(const WgradXCall& c) { return c.T == 0 || product_reach(grad_product(c)); }
 
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s) {
   if (c.T == 0) return hipSuccess;

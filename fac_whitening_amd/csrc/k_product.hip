@@ -878,6 +878,11 @@ bool as_it_is(const ProdOperand& m, int dtype, bool turned) {
   if (dtype == GIFT_FP32 || m.packed) return false;
   return turned ? m.near && m.cols % 2 == 0 : m.aligned && m.cols % 8 == 0;
 }
+// Whether k_product_pack has to lay an operand out, and can: of the four of a launch each has a quarter of its workgroups.
+bool to_pack(const ProdOperand& m, int dtype, bool turned) { return m.rows && !m.packed && !as_it_is(m, dtype, turned); }
+bool may_pack(const ProdOperand& m) {
+  return m.rows < ((int64_t)1 << 36) && cdiv(m.rows * cdiv(m.cols, 8), 256) <= kMaxGrid / 4;
+}
 
 }  // namespace
 
@@ -887,13 +892,26 @@ size_t product_packed(int dtype, int64_t rows, int64_t cols) {
   return align256((size_t)planes_of(dtype) * (size_t)rows * (size_t)packed_ld(cols) * 2);
 }
 
-// Workspace: the operands to pack, one after another, then the pieces.
+bool product_reach(const ProductCall& c) {
+  const bool ax = c.epi != kEpiGlu, bx = c.epi == kEpiGrad;
+  for (int i = 0; i < 2; ++i) {
+    if (to_pack(c.a[i], c.dtype, ax) && !may_pack(c.a[i])) return false;
+    if (to_pack(c.b[i], c.dtype, bx) && !may_pack(c.b[i])) return false;
+  }
+  return true;
+}
+
+// Workspace: the operands to pack, one after another, then the pieces.  (A query that knows less of the alignment than
+// the call counts nothing for an operand too large to pack: the call reads it as it is, or is refused.)
 size_t product_workspace(const ProductCall& c) {
   const bool ax = c.epi != kEpiGlu, bx = c.epi == kEpiGrad;
   size_t b = 0;
+  auto add = [&](const ProdOperand& m, bool turned) {
+    if (to_pack(m, c.dtype, turned) && may_pack(m)) b += product_packed(c.dtype, m.rows, m.cols);
+  };
   for (int i = 0; i < 2; ++i) {
-    if (c.a[i].rows && !c.a[i].packed && !as_it_is(c.a[i], c.dtype, ax)) b += product_packed(c.dtype, c.a[i].rows, c.a[i].cols);
-    if (c.b[i].rows && !c.b[i].packed && !as_it_is(c.b[i], c.dtype, bx)) b += product_packed(c.dtype, c.b[i].rows, c.b[i].cols);
+    add(c.a[i], ax);
+    add(c.b[i], bx);
   }
   return b + align256(product_plan(c.epi, ax, bx, c.M, c.N, c.K, c.parts * (c.dtype == GIFT_FP32 ? 6 : 1)).bytes);
 }

@@ -191,6 +191,7 @@ constexpr int64_t kProductRow = (int64_t)1 << 22;   // bytes: 256 rows' offsets 
 int64_t product_tiles(int64_t M, int64_t N);
 size_t product_packed(int dtype, int64_t rows, int64_t cols);   // bytes of an operand laid out anew
 size_t product_workspace(const ProductCall& c);
+bool product_reach(const ProductCall& c);                      // whether one launch lays out what has to be
 hipError_t launch_product(const ProductCall& c, const DropArgs& drop, hipStream_t s);
 
 }  // namespace gift

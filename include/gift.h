@@ -538,7 +538,8 @@ gift_status gift_dropout_apply(const gift_dropout* h_drop, const void* d_x, int3
  *   z = x Wg^T, u = x Wu^T, h = D(act(z) u)
  * act(z): silu z s(z), gelu z N(z) (N the normal distribution function), gelu_tanh z s(2 sqrt(2 / pi) (z + 0.044715
  * z^3)), relu max(z, 0), sigmoid s(z), with s(z) = 1 / (1 + e^-z).
- * Products take d, f and m up to 2^21 (GIFT_ERR_UNSUPPORTED beyond). */
+ * Products take d, f and m up to 2^21, and operands that have to be laid out anew (see gift_glu_workspace_bytes) up to
+ * 2^29 - 256 groups of eight columns, rows times ceil(columns / 8) (GIFT_ERR_UNSUPPORTED beyond). */
 enum gift_act { GIFT_ACT_SILU = 0, GIFT_ACT_GELU = 1, GIFT_ACT_GELU_TANH = 2, GIFT_ACT_RELU = 3, GIFT_ACT_SIGMOID = 4 };
 /* h, from the fp32 sums z and u, is rounded once to `dtype`.  d_gate, d_up [T][f] (both or neither): z and u rounded
  * to `dtype`, for the backward pass.  h_drop: NULL for none.  h_ckpt: h [T][f] as it was rounded is also saved there.
