@@ -814,14 +814,12 @@ def weight_grad(delta: torch.Tensor, ckpt, alpha: float = 1.0, out=None, accumul
         ldw = _rows(out, "out", m, d, torch.float32, dev)
     if whole:
         dp, xp = delta.data_ptr(), ckpt.data_ptr()
-        wbytes = _lib.gift_weight_grad_x_workspace_bytes(T, m, d, dt, _rows16(dt, (dp, ld, T), (xp, ldx, T)))
-    else:
-        wbytes = _lib.gift_weight_grad_workspace_bytes(T, m, d, dt)
-    work, wp, wbytes = _workspace(stream, work, wbytes, dev)
-    if whole:
+        work, wp, wbytes = _workspace(stream, work, dev, lambda: _lib.gift_weight_grad_x_workspace_bytes(
+            T, m, d, dt, _rows16(dt, (dp, ld, T), (xp, ldx, T))))
         _check(_lib.gift_weight_grad_x(dp, dt, ld, m, xp, ldx, T, d, alpha, int(accumulate), out.data_ptr(), ldw, wp,
                                        wbytes, raw), "gift_weight_grad_x")
     else:
+        work, wp, wbytes = _workspace(stream, work, dev, lambda: _lib.gift_weight_grad_workspace_bytes(T, m, d, dt))
         _check(_lib.gift_weight_grad(delta.data_ptr(), dt, ld, m, ckpt._ref, T, d, alpha, int(accumulate),
                                      out.data_ptr(), ldw, wp, wbytes, raw), "gift_weight_grad")
     return out
@@ -838,10 +836,12 @@ def _rows16(dt, *rows):
     return 1
 
 
-def _workspace(stream, work, nbytes, device):
-    """The given workspace, or a new one of nbytes (none for 0): tensor, address, bytes."""
+def _workspace(stream, work, device, size):
+    """The given workspace, or a new one of size() bytes (none for 0; asked only then, it takes 1 to 2 us): tensor,
+    address, bytes."""
     if work is not None:
         return work, work.data_ptr(), _bytes(device, work, "work")
+    nbytes = size()
     if nbytes == 0:
         return None, None, 0
     work = _empty(stream, (nbytes,), torch.uint8, device)
@@ -941,8 +941,8 @@ def glu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act="
     else:
         ldz = ldup = 0
     t, xp, gp, wp = DTYPES[dt], x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
-    work, kp, wbytes = _workspace(stream, work, _lib.gift_glu_workspace_bytes(
-        T, d, f, t, _rows16(t, (xp, ld, T), (gp, ldg, f), (wp, ldu, f))), dev)
+    work, kp, wbytes = _workspace(stream, work, dev, lambda: _lib.gift_glu_workspace_bytes(
+        T, d, f, t, _rows16(t, (xp, ld, T), (gp, ldg, f), (wp, ldu, f))))
     _check(_lib.gift_glu_forward(act, xp, t, ld, T, d, gp, ldg, wp, ldu, f, ref, out.data_ptr(), ldh,
                                  None if gate is None else gate.data_ptr(), ldz, None if up is None else up.data_ptr(),
                                  ldup, None if ckpt is None else ckpt._ref, kp, wbytes, raw), "gift_glu_forward")
@@ -974,7 +974,7 @@ def glu_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, w_gate=
         lddup = _rows(dup, "dup", T, f, dt, dev)
     t, zp, up_ = DTYPES[dt], dgate.data_ptr(), dup.data_ptr()
     if w_gate is None:
-        d = ldg = ldu = lddx = nbytes = 0
+        d = ldg = ldu = lddx = 0
         gp = wp = xp = None
     else:
         ldg, d = _rows(w_gate, "w_gate", f, None, dt, dev), w_gate.shape[1]
@@ -984,10 +984,10 @@ def glu_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, w_gate=
         else:
             lddx = _rows(dx, "dx", T, d, dt, dev)
         gp, wp, xp = w_gate.data_ptr(), w_up.data_ptr(), dx.data_ptr()
-        nbytes = _lib.gift_glu_backward_workspace_bytes(
+    work, kp, wbytes = _workspace(stream, work, dev, lambda: 0 if w_gate is None else (
+        _lib.gift_glu_backward_workspace_bytes(
             T, d, f, t, int((lddz == lddup or T == 1) and (ldg == ldu or f == 1) and
-                            _rows16(t, (zp, lddz, T), (up_, lddup, T), (gp, ldg, f), (wp, ldu, f))))
-    work, kp, wbytes = _workspace(stream, work, nbytes, dev)
+                            _rows16(t, (zp, lddz, T), (up_, lddup, T), (gp, ldg, f), (wp, ldu, f))))))
     _check(_lib.gift_glu_backward(act, dh.data_ptr(), t, ld, T, f, gate.data_ptr(), ldz, up.data_ptr(), ldup, ref, zp,
                                   lddz, up_, lddup, gp, ldg, wp, ldu, d, xp, lddx, kp, wbytes, raw), "gift_glu_backward")
     return dx, dgate, dup
