@@ -349,18 +349,8 @@ size_t wgrad_x_workspace(const WgradXCall& c);
 bool glu_forward_reach(const GluCall& c);
 bool glu_backward_reach(const GluGradCall& c);
 bool wgrad_x_reach(const WgradXCall& c);
-// Whether k_glu_tokens makes the block's output: up to 32 rows of x, and up to 64 where the weights are small (tokens
-// against tiles, 64 rows bf16: 1536 x 6144 22 and 23 us, 4096 x 16384 111 and 68) or fp32, whose tiles need their
-// operands laid out anew (1536 x 6144: 64 and 88).
-inline bool glu_by_tokens(int dtype, int64_t T, int d, int f) {
-  return T <= 32 || (T <= 64 && (dtype == GIFT_FP32 || (int64_t)d * f <= (int64_t)1 << 24));
-}
 hipError_t launch_glu_tokens(const GluCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s);
-// Whether the tokens' backward form runs: dx asked for, few rows, and no output over what it reads again.
-inline bool glu_backward_by_tokens(const GluGradCall& c) {
-  return c.T <= (c.dtype == GIFT_FP32 ? 16 : 32) && !c.in_place;
-}
 size_t glu_tokens_backward_workspace(int64_t T, int d, int f);
 hipError_t launch_glu_tokens_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s);
 hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s);

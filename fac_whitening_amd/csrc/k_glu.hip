@@ -166,12 +166,12 @@ ProductCall grad_product(const WgradXCall& c) {
 size_t glu_forward_workspace(const GluCall& c) { return glu_by_tokens(c.dtype, c.T, c.d, c.f) ? 0 : product_workspace(glu_product(c)); }
 size_t glu_backward_workspace(const GluGradCall& c) {
   if (c.T == 0) return 0;
-  if (glu_backward_by_tokens(c)) return glu_tokens_backward_workspace(c.T, c.d, c.f);
+  if (glu_backward_by_tokens(c.dtype, c.T, c.in_place)) return glu_tokens_backward_workspace(c.T, c.d, c.f);
   return product_workspace(dx_product(c)) + (gradients_packed(c) ? 2 * product_packed(c.dtype, c.T, c.f) : 0);
 }
 size_t wgrad_x_workspace(const WgradXCall& c) { return c.T ? product_workspace(grad_product(c)) : 0; }
 bool glu_forward_reach(const GluCall& c) { return glu_by_tokens(c.dtype, c.T, c.d, c.f) || product_reach(glu_product(c)); }
-bool glu_backward_reach(const GluGradCall& c) { return glu_backward_by_tokens(c) || product_reach(dx_product(c)); }
+bool glu_backward_reach(const GluGradCall& c) { return glu_backward_by_tokens(c.dtype, c.T, c.in_place) || product_reach(dx_product(c)); }
 bool wgrad_x_reach(const WgradXCall& c) { return c.T == 0 || product_reach(grad_product(c)); }
 
 hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_t s) {
@@ -181,7 +181,7 @@ hipError_t launch_glu_forward(const GluCall& c, const DropArgs& drop, hipStream_
 
 hipError_t launch_glu_backward(const GluGradCall& c, const DropArgs& drop, hipStream_t s) {
   if (c.T == 0) return hipSuccess;
-  if (c.dx && glu_backward_by_tokens(c)) return launch_glu_tokens_backward(c, drop, s);
+  if (c.dx && glu_backward_by_tokens(c.dtype, c.T, c.in_place)) return launch_glu_tokens_backward(c, drop, s);
   uint16_t* planes[2] = {nullptr, nullptr};
   if (c.dx && gradients_packed(c)) {
     planes[0] = static_cast<uint16_t*>(c.work);

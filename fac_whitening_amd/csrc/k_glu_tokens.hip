@@ -153,10 +153,8 @@ namespace {
 template <typename T, int ACT, int NT>
 void tokens_rows(const GluCall& c, const DropArgs& drop, hipStream_t s) {
   const dim3 block(64 * kTokenWaves);
-  // 32 hidden units a workgroup read x half as often.  4096 x 16384 bf16, 16 units against 32: 1 token 52 and 57 us, 16
-  // tokens 65 and 61, 32 tokens 79 and 69; with fewer than two workgroups a compute unit the smaller ones are quicker.
   if constexpr (sizeof(T) == 2 && NT < 4)
-    if (c.T > 8 && cdiv(c.f, 32) >= 512) {
+    if (glu_token_units(c.dtype, c.T, c.f) == 2) {
       hipLaunchKernelGGL((k_glu_tokens<T, ACT, NT, 2>), dim3((unsigned)cdiv(c.f, 32)), block, 0, s, c, drop);
       return;
     }

@@ -85,43 +85,18 @@ __device__ __forceinline__ DropArgs drop_args_of(ConstOut& o) {
   return d;
 }
 
-// Piece p of workgroup g (the p-th call of wgrad_walk): tile, stages, number.
+// Piece p of workgroup g: tile, stages, number.
 struct Piece {
   int tile, s0, s1, number;
 };
 __device__ __forceinline__ bool product_piece(const ConstArgs* a, int g, int p, Piece& out) {
   const int total = a->nst * a->nseg, unit = a->unit;
-  WLevel v = wgrad_levels(a->nbm * a->nbn, (total + unit - 1) / unit, gridDim.x);
-  for (; !v.done(); v.next()) {
-    int from = v.from, units;
-    if (v.split()) {
-      const int mine = v.count() * v.R;
-      if (g >= mine) {
-        g -= mine;
-        continue;
-      }
-      if (p > 0) return false;
-      const int c = g / v.R;
-      out.tile = v.tile0 + g - c * v.R;
-      from += c * v.C;
-      units = v.C;
-      out.number = v.base + g;
-    } else {
-      const int n = g >= v.R ? 0 : (v.R - g + v.W - 1) / v.W;      // of this level's tiles
-      const int mine = n < v.count() ? n : v.count();
-      if (p >= mine) {
-        p -= mine;
-        continue;
-      }
-      out.tile = v.tile0 + g + p * v.W;
-      units = v.n;
-      out.number = v.base + g + p * v.W;
-    }
-    out.s0 = from * unit;
-    out.s1 = out.s0 + units * unit < total ? out.s0 + units * unit : total;
-    return true;
-  }
-  return false;
+  int from, units;
+  if (!wgrad_piece(wgrad_levels(a->nbm * a->nbn, (total + unit - 1) / unit, gridDim.x), g, p, out.tile, from, units, out.number))
+    return false;
+  out.s0 = from * unit;
+  out.s1 = out.s0 + units * unit < total ? out.s0 + units * unit : total;
+  return true;
 }
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -768,68 +743,6 @@ __global__ void __launch_bounds__(256) k_product_pack(PackArgs a) {
 }
 
 namespace {
-
-constexpr int kProductGroups = 256;   // compute units of an MI355X
-
-struct ProdPlan {
-  int side, deep, nbm, nbn, nst, unit, grid;   // deep: four stages in LDS, one workgroup a compute unit
-  int first, split;    // first split tile, split tiles
-  size_t bytes;        // of the pieces
-};
-
-// A plan in one of three forms (tiles of 256, of 128 with two workgroups a
-// compute unit, of 128 with one and four stages in LDS), split at multiples of
-// `unit` stages (0: not split), and what it is expected to take, in us.
-// Measured on bf16 (direct x direct, transposing x direct, both transposing; 1536
-// x 6144 and 4096 x 4096, 128 to 8192 tokens), within a fifth or so:
-//   a stage of a workgroup   256: 1.75 each; 128: 1.0, 1.25, 1.15; deep: 0.6
-//   a whole tile written     256: 6, fp32 gradients 14; 128: 2, 4
-//   a split                  7 for the launch of the join, pieces written and read at 8 TB/s, outputs written at 6, and
-//                            0.15 for each piece of a tile, which the join adds one after another
-double product_try(ProdPlan& p, int side, int deep, int unit, int most, int epi, bool ax, bool bx, int64_t M, int64_t N, int64_t K, int nseg) {
-  p.side = side;
-  p.deep = deep;
-  p.nbm = (int)cdiv(M, epi == kEpiGlu ? side / 2 : side);
-  p.nbn = (int)cdiv(N, side);
-  p.nst = (int)cdiv(K, 64);
-  p.grid = side == 128 && !deep ? 2 * kProductGroups : kProductGroups;
-  const int total = p.nst * nseg;
-  p.unit = unit ? unit : total;
-  const int64_t tiles = (int64_t)p.nbm * p.nbn;
-  if (unit && tiles * most < p.grid) p.grid = (int)tiles * most;
-  const WLevel v = wgrad_levels((int)tiles, (int)cdiv(total, p.unit), p.grid);
-  const WSplit w = wgrad_split(v);
-  p.first = w.first;
-  p.split = w.tiles;
-  p.bytes = (size_t)w.pieces * side * side * 4;
-  const double stages = (double)v.C * p.unit;
-  const bool large = side == 256, grad = epi == kEpiGrad;
-  const double stage = large ? 1.75 : deep ? 0.6 : bx ? 1.15 : ax ? 1.25 : 1.0;
-  const double whole = (double)(v.C * (int64_t)p.unit / total) * (large ? grad ? 14.0 : 6.0 : grad ? 4.0 : 2.0);
-  const double join = 7.0 + 2.0 * (double)p.bytes / 8e6 + 0.15 * (double)cdiv(p.grid, tiles) +
-                      (double)p.split * side * side * (grad ? 4 : 2) / 6e6;
-  return stages * stage + whole + (p.split ? join : 0.0);
-}
-
-ProdPlan product_plan(int epi, bool ax, bool bx, int64_t M, int64_t N, int64_t K, int nseg) {
-  ProdPlan best{};
-  double least = 0;
-  if (K < 1) return best;
-  for (int form = 0; form < 3; ++form) {   // 256, 128, 128 deep
-    if (form == 2 && (ax || bx)) continue;
-    for (int unit = 0; unit <= 8; unit += unit ? unit : 2)
-      for (int most = 4; most <= 256; most *= 4) {   // workgroups a tile
-        ProdPlan p{};
-        const double t = product_try(p, form == 0 ? 256 : 128, form == 2, unit, most, epi, ax, bx, M, N, K, nseg);
-        if (best.side == 0 || t < least) {
-          best = p;
-          least = t;
-        }
-        if (unit == 0) break;
-      }
-  }
-  return best;
-}
 
 template <typename E, typename TO, int EPI, int ACT, bool AX, bool BX>
 void product_go(const ProdArgs& a, const ProdOut& o, const ProdPlan& p, hipStream_t s) {

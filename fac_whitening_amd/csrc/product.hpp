@@ -4,7 +4,7 @@
 #include <type_traits>
 
 #include "glu.hpp"
-#include "wgrad_levels.hpp"
+#include "product_plan.hpp"
 
 namespace gift {
 
@@ -154,8 +154,6 @@ struct ProdArgs {
   int nbm, nbn, unit;   // tiles along i and j; tiles are split at multiples of `unit` stages
   float* part;          // pieces of split tiles
 };
-
-enum { kEpiGlu = 0, kEpiStore = 1, kEpiGrad = 2 };
 
 struct ProdOut {
   void *out, *gate, *up;

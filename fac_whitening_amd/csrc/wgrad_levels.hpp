@@ -91,6 +91,39 @@ __host__ __device__ inline void wgrad_walk(WLevel v, int g, U&& uniform, F&& pie
   }
 }
 
+// Piece p of workgroup g, the p-th that wgrad_walk calls for; false past the
+// last.  (For a kernel that asks for one piece at a time.)
+__host__ __device__ inline bool wgrad_piece(WLevel v, int g, int p, int& tile, int& from, int& units, int& number) {
+  for (; !v.done(); v.next()) {
+    from = v.from;
+    if (v.split()) {
+      const int mine = v.count() * v.R;
+      if (g >= mine) {
+        g -= mine;
+        continue;
+      }
+      if (p > 0) return false;
+      const int c = g / v.R;
+      tile = v.tile0 + g - c * v.R;
+      from += c * v.C;
+      units = v.C;
+      number = v.base + g;
+    } else {
+      const int n = g >= v.R ? 0 : (v.R - g + v.W - 1) / v.W;      // of this level's tiles
+      const int mine = n < v.count() ? n : v.count();
+      if (p >= mine) {
+        p -= mine;
+        continue;
+      }
+      tile = v.tile0 + g + p * v.W;
+      units = v.n;
+      number = v.base + g + p * v.W;
+    }
+    return true;
+  }
+  return false;
+}
+
 // Calls add(number, stride, count) for each level's numbered pieces of a split
 // tile, in token order: number, number + stride, ...
 template <typename F>
