@@ -7,8 +7,9 @@
 // On v_mfma_f32_32x32x16 with fp32 sums.  bf16 and fp16 operands multiply
 // exactly.  An fp32 operand is three bf16 planes (split_planes) and the long
 // axis six segments, the products of planes (0, 2), (1, 1), (2, 0), (0, 1), (1,
-// 0), (0, 0): what is left out is below 2^-24 of |A| |B|, and the small products
-// are added before the large ones.
+// 0), (0, 0): what is left out is below 2^-24 of |A| |B| (and of operands below
+// 2^-110 what lies under 2^-133), and the small products are added before the
+// large ones.
 //
 // One workgroup (4 waves, 2 x 2) makes a tile of 256 x 256, or 128 x 128, in
 // stages of 64 of the long axis; of kEpiGlu half of A's rows are the gate's,

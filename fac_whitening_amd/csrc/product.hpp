@@ -28,7 +28,8 @@ using Frag8 = std::conditional_t<std::is_same<E, Fp16>::value, pf16x8, pbf16x8>;
 // Three bf16 numbers whose sum is v, each the nearest to what the ones before
 // it leave: put(plane, four words of eight values).  (The first is at most the
 // largest bf16 number, which values beyond it would round past; of an infinity
-// or NaN at least one is not finite.)
+// or NaN at least one is not finite.  Bits below 2^-133, the smallest bf16
+// number, are lost: v below 2^-110 may have some.)
 template <typename F>
 __device__ __forceinline__ void split_planes(float* v, F&& put) {
 #pragma unroll

@@ -498,8 +498,9 @@ gift_status gift_weight_grad(const void* d_delta, int32_t dtype, int64_t ldd, in
 
 /* W = alpha delta^T x (+ W when accumulate != 0) as gift_weight_grad, from an activation x [T][ldx] of delta's type
  * that was kept whole.  bf16 and fp16 products are exact in the fp32 sums.  An fp32 operand is the sum of three bf16
- * numbers, of whose nine products the six largest are added: what is left out is below 2^-24 of |delta| |x|; an
- * infinity in an fp32 operand may give NaN, where IEEE arithmetic gives an infinity.  Sums are fp32, in the same order on every call.
+ * numbers, of whose nine products the six largest are added: what is left out is below 2^-24 of |delta| |x| (and of
+ * operands below 2^-110, as in gift_weight_grad, what lies under 2^-133 is dropped); an infinity in an fp32 operand may
+ * give NaN, where IEEE arithmetic gives an infinity.  Sums are fp32, in the same order on every call.
  * d_W may not overlap delta or x.  Workspace and `aligned` (of delta and x): see gift_glu_forward. */
 size_t gift_weight_grad_x_workspace_bytes(int64_t T, int32_t m, int32_t d, int32_t dtype, int32_t aligned);
 gift_status gift_weight_grad_x(const void* d_delta, int32_t dtype, int64_t ldd, int32_t m, const void* d_x,
