@@ -1,8 +1,10 @@
 // Gated block of few tokens (a decoding step): h = D(act(x Wg^T) (x Wu^T)) for
-// few rows of x (glu_by_tokens).  Every weight is read once, and the memory
+// few rows of x (glu_by_tokens).  Every weight is read once (33 to 64 fp32 tokens
+// run as two sets, 32 tokens and the rest, and read them twice), and the memory
 // pipe is what bounds it.
 //
-// A workgroup of 8 waves makes 16 hidden units of all tokens.  The waves share
+// A workgroup of 8 waves makes 16 hidden units of all tokens of a set, or 32
+// (glu_token_units).  The waves share
 // the long axis in blocks of 64: a lane loads 16 bytes of a weight row (16 rows x 64
 // bytes a load; rows may start anywhere) straight into the operand of
 // v_mfma_f32_16x16x32, tokens being the other operand, in 16s.  The next block's
@@ -10,7 +12,7 @@
 // meet in LDS and are added in order.  fp32 operands are split into three bf16
 // numbers in registers (split_planes); six products are added.
 // Measured: 1 token, 1536 x 6144 bf16 9.7 us (weights at a copy's rate 6.1), fp32
-// 23 (12.2); 16 tokens, 4096 x 16384 bf16 58 us (43.5; 4.6 TB/s).  A wave has 8 to 16 KB
+// 23 (12.2), 64 tokens fp32 45; 16 tokens, 4096 x 16384 bf16 58 us (43.5; 4.6 TB/s).  A wave has 8 to 16 KB
 // of loads in flight; what is left is the loads of x, which every workgroup
 // repeats, and the sums' way through LDS.
 #include "product.hpp"

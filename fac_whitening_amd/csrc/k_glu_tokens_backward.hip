@@ -9,11 +9,16 @@
 // v_mfma_f32_16x16x32 number c, whose 16 rows are columns c, 8 + c, ..., so that no
 // LDS is needed.  The other operand is 8 units of a token, which the lane computes
 // from dh, z and u, rounded as dgate and dup are (the workgroups of the first
-// columns store them).  The waves' sums meet in LDS, the slabs' in the
+// columns store them): dx is the product of the gradients that the weight
+// gradients see, and 16-bit ones enter the matrix cores as they are.  The waves'
+// sums meet in LDS, the slabs' in the
 // workspace; both are added in order, the latter by a second launch.  fp32
 // operands are split into three bf16 numbers in registers.
 // Measured: 1 token, 91 x 16173 fp32 12 + 3 us of kernels (as tiles with their join
-// 18 + 73); 2 tokens, 73 x 2752 bf16 9 + 3.
+// 18 + 73); 2 tokens, 73 x 2752 bf16 9 + 3; 16 tokens in all, us and a copy's time of
+// the weights: 1536 x 6144 bf16 20 and 6, fp32 33 and 13, 4096 x 16384 bf16 62 and 44,
+// fp32 114 and 88 (17 fp32 tokens, as tiles of planes laid out in memory: 88 and 520).
+// A step's loads are waited for before its products.
 #include "product.hpp"
 
 namespace gift {

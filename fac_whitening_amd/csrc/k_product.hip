@@ -40,8 +40,8 @@
 //    of split tiles joined in the order of the long axis by a second launch.
 // Measured (bf16): 8192^3 1.28 PFLOP/s direct, 1.20 transposing (a library
 // product 1.37, the clock then bound by power); 16384 tokens, 1536 x 6144:
-// forward 568 us, with both products kept and dropout 657, dx 530, weight
-// gradient 291.  Of dx, the matrix units are busy 59 % of 1.0 million clocks at 1.92
+// forward 568 to 576 us, with dropout 31 more, with both products kept 69 more,
+// both 657 to 677 (machines differ), dx 530, weight gradient 291.  Of dx, the matrix units are busy 59 % of 1.0 million clocks at 1.92
 // GHz; waves wait for counters and barriers 19 % of the time.  An earlier
 // barrier with all operands of a stage read at its start, and reads spread over
 // all products, took the same time.

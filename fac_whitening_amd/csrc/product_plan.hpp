@@ -13,7 +13,7 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whether k_glu_tokens makes the block's output: up to 32 rows of x, and up to 64 where the weights are small (tokens
 // against tiles, 64 rows bf16: 1536 x 6144 22 and 23 us, 4096 x 16384 111 and 68) or fp32, whose tiles need their
-// operands laid out anew (1536 x 6144: 64 and 88).
+// operands laid out anew (1536 x 6144: 45 and 86; the limit of 2^24 weights lies between the two shapes).
 inline bool glu_by_tokens(int dtype, int64_t T, int d, int f) {
   return T <= 32 || (T <= 64 && (dtype == GIFT_FP32 || (int64_t)d * f <= (int64_t)1 << 24));
 }
@@ -23,7 +23,9 @@ inline bool glu_by_tokens(int dtype, int64_t T, int d, int f) {
 inline int glu_token_units(int dtype, int64_t T, int f) {
   return dtype != GIFT_FP32 && T > 8 && T <= 32 && ceil_div(f, 32) >= 512 ? 2 : 1;
 }
-// Whether the tokens' backward form makes dx: few rows, and no output over what it reads again.
+// Whether the tokens' backward form makes dx: few rows, and no output over what it reads again.  (It is
+// built for two sets of 16 tokens in 16 bits and for one in fp32.  The tiles behind it, 33 rows bf16 against 32: 1536 x 6144
+// 33 and 25 us, 4096 x 16384 72 and 70; fp32, 17 against 16: 88 and 33, 520 and 114.)
 inline bool glu_backward_by_tokens(int dtype, int64_t T, bool in_place) {
   return T <= (dtype == GIFT_FP32 ? 16 : 32) && !in_place;
 }
@@ -42,7 +44,8 @@ struct ProdPlan {
 // compute unit, of 128 with one and four stages in LDS), split at multiples of
 // `unit` stages (0: not split), and what it is expected to take, in us.
 // Measured on bf16 (direct x direct, transposing x direct, both transposing; 1536
-// x 6144 and 4096 x 4096, 128 to 8192 tokens), within a fifth or so:
+// x 6144 and 4096 x 4096, 128 to 8192 tokens), within a fifth or so, and taken for
+// fp32 too, whose stages are the same over six times as many:
 //   a stage of a workgroup   256: 1.75 each; 128: 1.0, 1.25, 1.15; deep: 0.6
 //   a whole tile written     256: 6, fp32 gradients 14; 128: 2, 4
 //   a split                  7 for the launch of the join, pieces written and read at 8 TB/s, outputs written at 6, and
