@@ -41,10 +41,11 @@
 // Measured (bf16): 8192^3 1.28 PFLOP/s direct, 1.20 transposing (a library
 // product 1.37, the clock then bound by power); 16384 tokens, 1536 x 6144:
 // forward 568 to 576 us, with dropout 31 more, with both products kept 69 more,
-// both 657 to 677 (machines differ), dx 530, weight gradient 291.  Of dx, the matrix units are busy 59 % of 1.0 million clocks at 1.92
-// GHz; waves wait for counters and barriers 19 % of the time.  An earlier
-// barrier with all operands of a stage read at its start, and reads spread over
-// all products, took the same time.
+// both 657 to 677 (machines differ), dx 530, weight gradient 291.  Of dx, the
+// matrix units are busy 59 % of 1.0 million clocks at 1.92 GHz; waves wait for
+// counters and barriers 19 % of the time.  An earlier barrier with all operands of
+// a stage read at its start, and reads spread over all products, took the same
+// time.
 #include "product.hpp"
 
 namespace gift {
@@ -93,8 +94,8 @@ struct Piece {
 __device__ __forceinline__ bool product_piece(const ConstArgs* a, int g, int p, Piece& out) {
   const int total = a->nst * a->nseg, unit = a->unit;
   int from, units;
-  if (!wgrad_piece(wgrad_levels(a->nbm * a->nbn, (total + unit - 1) / unit, gridDim.x), g, p, out.tile, from, units, out.number))
-    return false;
+  const WLevel v = wgrad_levels(a->nbm * a->nbn, (total + unit - 1) / unit, gridDim.x);
+  if (!wgrad_piece(v, g, p, out.tile, from, units, out.number)) return false;
   out.s0 = from * unit;
   out.s1 = out.s0 + units * unit < total ? out.s0 + units * unit : total;
   return true;
